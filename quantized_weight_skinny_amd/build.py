@@ -1,4 +1,5 @@
-"""Build libqpn.so (the HIP kernels and the C ABI of include/qpn.h) for gfx950.
+"""Build libqpn.so (the HIP kernels and the C ABI of include/qpn.h and
+include/qpn_decode.h) for gfx950.
 
 Run ``python -m quantized_weight_skinny_amd.build`` (or call ``build()``); the
 library lands next to this file so that it travels with the source tree.
@@ -11,7 +12,9 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
-SOURCES = ["qpn_api.hip", "qpn_gemm.hip", "qpn_mlp.hip", "qpn_pack.hip", "qpn_plan.cpp", "qpn_checks.cpp"]
+SOURCES = ["qpn_api.hip", "qpn_gemm.hip", "qpn_mlp.hip", "qpn_pack.hip", "qpn_plan.cpp", "qpn_checks.cpp",
+           "qpn_decode_api.hip", "qpn_kv4_attention.hip", "qpn_kv4_cache.hip", "qpn_verify.hip",
+           "qpn_decode_checks.cpp"]
 LIB = os.path.join(HERE, "libqpn.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -23,6 +26,7 @@ FLAGS = [
     "-fPIC",
     "-shared",
     "-Wall",
+    "-parallel-jobs=8",
     # keep the compiler from forming packed fp32 (v_pk_*_f32) instructions
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-I", os.path.join(ROOT, "include"),

@@ -93,7 +93,7 @@ qpn_status plan_attention(const qpn_kv4_cache* c, const qpn_kv4_attention_args* 
   if (a->max_kv_len < 0 || a->max_kv_len > (1 << 30) || a->window < 0) return QPN_ERR_INVALID_ARG;
   const int64_t rows = static_cast<int64_t>(std::min(a->max_q_len, a->rows)) * (a->heads / c->kv_heads);
   const int64_t t16 = std::max<int64_t>(1, (rows + 15) / 16);
-  const int most = c->head_dim == 256 ? 2 : 4;
+  const int most = c->head_dim == 256 ? 2 : c->head_dim == 128 ? 3 : 4;
   p->row_tiles = static_cast<int>((t16 + most - 1) / most);
   p->tiles16 = static_cast<int>((t16 + p->row_tiles - 1) / p->row_tiles);
   p->row_tiles = static_cast<int>((t16 + p->tiles16 - 1) / p->tiles16);

@@ -90,57 +90,89 @@ struct Tile {
   uint32_t k[2][kWords], v[2][kWords], ks[2], vs[2];
 };
 
+// A page's segment, read with raw buffer loads: its base and range and the
+// place of a half in it sit in scalar registers, a lane's offsets do not
+// change, so an address costs no vector instruction; and nothing past the
+// segment can be read.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t segment_of(const uint8_t* seg, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(seg), 0, bytes, Stream::kRsrcWord3);
+}
+
 template <int WORDS>
-__device__ __forceinline__ void load_words(uint32_t (&r)[WORDS], const uint8_t* p) {
+__device__ __forceinline__ void load_words(uint32_t (&r)[WORDS], __amdgpu_buffer_rsrc_t seg, int lane_at, int at) {
   if constexpr (WORDS == 2) {
-    typedef uint32_t u2 __attribute__((ext_vector_type(2)));
-    const u2 x = __builtin_nontemporal_load(reinterpret_cast<const u2*>(p));
+    const auto x = __builtin_amdgcn_raw_buffer_load_b64(seg, lane_at, at, Stream::kStreaming);
     r[0] = x[0], r[1] = x[1];
   } else {
 #pragma unroll
     for (int j = 0; j < WORDS / 4; ++j) {
-      const u4 x = __builtin_nontemporal_load(reinterpret_cast<const u4*>(p) + j);
+      const u4 x = __builtin_amdgcn_raw_buffer_load_b128(seg, lane_at + 16 * j, at, Stream::kStreaming);
 #pragma unroll
       for (int e = 0; e < 4; ++e) r[4 * j + e] = x[e];
     }
   }
 }
 
-// Half `h` (16 tokens from offset `off` of a page's segment `seg`).
+// Half `h` (16 tokens from offset `off` of a page's segment `seg`): the keys,
+// and the values.
 template <int DIM>
-__device__ __forceinline__ void load_half(Tile<DIM>& t, int h, const uint8_t* seg, int off, int page, int lane) {
+__device__ __forceinline__ void load_keys(Tile<DIM>& t, int h, __amdgpu_buffer_rsrc_t seg, int off, int page, int lane) {
   const int i = lane & 15, g = lane >> 4;
-  const uint8_t* k = seg + off * (DIM / 2);
-  const uint8_t* v = seg + page * (DIM / 2) + off * (DIM / 2);
-  const uint8_t* ks = seg + page * DIM + off * (DIM / 16);
-  const uint8_t* vs = seg + page * DIM + page * (DIM / 16) + off * (DIM / 16);
-  load_words(t.k[h], k + static_cast<uint32_t>(i * (DIM / 2) + g * (DIM / 8)));
-  load_words(t.v[h], v + static_cast<uint32_t>(lane_v<DIM>(i, g)));
-  const uint32_t ko = i * (DIM / 16) + g * (DIM / 64);
+  load_words(t.k[h], seg, i * (DIM / 2) + g * (DIM / 8), off * (DIM / 2));
+  const int lane_at = i * (DIM / 16) + g * (DIM / 64), at = page * DIM + off * (DIM / 16);
   if constexpr (DIM == 64)
-    t.ks[h] = ks[ko];
+    t.ks[h] = __builtin_amdgcn_raw_buffer_load_b8(seg, lane_at, at, Stream::kStreaming);
   else if constexpr (DIM == 128)
-    t.ks[h] = *reinterpret_cast<const uint16_t*>(ks + ko);
+    t.ks[h] = __builtin_amdgcn_raw_buffer_load_b16(seg, lane_at, at, Stream::kStreaming);
   else
-    t.ks[h] = *reinterpret_cast<const uint32_t*>(ks + ko);
-  t.vs[h] = *reinterpret_cast<const uint32_t*>(vs + static_cast<uint32_t>(g * (DIM / 4) + (i * DIM / 256) * 4));
+    t.ks[h] = __builtin_amdgcn_raw_buffer_load_b32(seg, lane_at, at, Stream::kStreaming);
+}
+
+template <int DIM>
+__device__ __forceinline__ void load_vals(Tile<DIM>& t, int h, __amdgpu_buffer_rsrc_t seg, int off, int page, int lane) {
+  const int i = lane & 15, g = lane >> 4;
+  load_words(t.v[h], seg, lane_v<DIM>(i, g), page * (DIM / 2) + off * (DIM / 2));
+  t.vs[h] = __builtin_amdgcn_raw_buffer_load_b32(seg, g * (DIM / 4) + (i * DIM / 256) * 4,
+                                                 page * DIM + page * (DIM / 16) + off * (DIM / 16), Stream::kStreaming);
+}
+
+// The larger of three (two). The compiler's fmaxf first quiets each operand
+// that it has not computed itself, an instruction each.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+__device__ __forceinline__ float max2(float a, float b) {
+  float r;
+  asm("v_max_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
 }
 
 __device__ __forceinline__ h2 splat(_Float16 x) { return h2{x, x}; }
 
-// S^T of 16 tokens against one 16-row tile per entry of `s`.
-template <int DIM, int NQ>
-__device__ __forceinline__ void scores(const Tile<DIM>& t, int h, const h8 (&q)[NQ][DIM / 32], f4 (&s)[NQ]) {
-  h2 sc[2];
-  sc[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(t.ks[h], 1.0f, false);
-  if constexpr (DIM == 256) sc[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(t.ks[h], 1.0f, true);
+// S^T of 32 tokens against the row tiles: step c of both halves meets each
+// query fragment q(n, c) once.
+template <int DIM, int NQ, typename Q>
+__device__ __forceinline__ void scores(const Tile<DIM>& t, const Q& q, f4 (&s)[2][NQ]) {
+  h2 sc[2][2];
 #pragma unroll
-  for (int n = 0; n < NQ; ++n) s[n] = f4{0.f, 0.f, 0.f, 0.f};
+  for (int h = 0; h < 2; ++h) {
+    sc[h][0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(t.ks[h], 1.0f, false);
+    if constexpr (DIM == 256) sc[h][1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(t.ks[h], 1.0f, true);
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) s[h][n] = f4{0.f, 0.f, 0.f, 0.f};
+  }
 #pragma unroll
   for (int c = 0; c < DIM / 32; ++c) {
-    const h8 k = decode_fp4x8(t.k[h][c], splat(sc[c / 4][(c / 2) & 1]));
+    const h8 k0 = decode_fp4x8(t.k[0][c], splat(sc[0][c / 4][(c / 2) & 1]));
+    const h8 k1 = decode_fp4x8(t.k[1][c], splat(sc[1][c / 4][(c / 2) & 1]));
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) s[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[n][c], s[n], 0, 0, 0);
+    for (int n = 0; n < NQ; ++n) {
+      const h8 x = q(n, c);
+      s[0][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, x, s[0][n], 0, 0, 0);
+      s[1][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, x, s[1][n], 0, 0, 0);
+    }
   }
 }
 
@@ -219,6 +251,12 @@ __device__ __forceinline__ void store_out8(void* out, int64_t at, const float (&
   *reinterpret_cast<u4*>(static_cast<uint16_t*>(out) + at) = w;
 }
 
+// Wavefronts a SIMD is to hold: the output tiles and what a step needs fit
+// 512 / waves registers (NQ * DIM / 4 of them for the output).
+constexpr int waves_per_simd(int dim, int nq) {
+  return dim == 256 || nq >= (dim == 64 ? 4 : 3) ? 2 : nq * dim <= 128 ? 4 : 3;
+}
+
 // Workgroup u takes unit u: of one sequence, a run of tiles, a row tile and a
 // kv head. The units are counted out on the device from the lengths, so a
 // captured call follows them: with `total` tiles to do over all sequences, row
@@ -227,11 +265,18 @@ __device__ __forceinline__ void store_out8(void* out, int64_t at, const float (&
 // workgroups read neighbouring segments of one page), then row tiles: with 8
 // heads or a multiple, the row tiles that read the same tokens land on the same XCD.
 template <int DIM, int NQ, bool BF16>
-__global__ __launch_bounds__(kW * 64) void kv4_attention_kernel(const AttnParams a) {
+__global__ __launch_bounds__(kW * 64, waves_per_simd(DIM, NQ)) void kv4_attention_kernel(const AttnParams a) {
   constexpr int kRows = 16 * NQ, kBlocks = DIM / 16, kSteps = DIM / 32;
   constexpr int kPad = DIM + 4;
-  __shared__ float red[kW][16][kPad];
+  constexpr bool kQueriesInLds = NQ * DIM > 128;
+  union Shared {
+    float red[kW][16][kPad];
+    u4 q[kQueriesInLds ? NQ * kSteps * 64 : 1];
+  };
+  __shared__ Shared sh;
   __shared__ float2 ml[kW][kRows];
+  __shared__ float fs[kRows];
+  auto& red = sh.red;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i = lane & 15, g = lane >> 4;
   const int unit = blockIdx.x;
@@ -247,7 +292,9 @@ __global__ __launch_bounds__(kW * 64) void kv4_attention_kernel(const AttnParams
   }
   total = wave_sum(total) * a.kv_heads;
   // no sequence is longer than 2^30 tokens: a chunk that is cut there holds any
-  const int chunk = max(a.min_chunk, static_cast<int>(min((total + a.slots - 1) / a.slots, 1ll << 26)));
+  // (the same in every lane: held in a scalar register, like all that follows from it)
+  const int chunk = __builtin_amdgcn_readfirstlane(
+      max(a.min_chunk, static_cast<int>(min((total + a.slots - 1) / a.slots, 1ll << 26))));
   int b = -1, base = 0, splits = 0;
   for (int b0 = 0, before = 0; b0 < a.batch; b0 += 64) {
     const int bl = b0 + lane;
@@ -283,23 +330,17 @@ __global__ __launch_bounds__(kW * 64) void kv4_attention_kernel(const AttnParams
   const int rtile = rest % s.rt, split = rest / s.rt;
   if (rest == 0 && head == 0 && tid == 0) a.sched[b] = int4{base, splits, s.rt, 0};
 
-  // Rows of this lane in each 16-row tile: query index (-1: none) and position.
+  // The rows: row r of the row tile is query row r / group, head r % group.
   const int row0 = rtile * kRows, nrows = min(s.ql * a.group - row0, kRows);
   int pos[NQ];
-  h8 q[NQ][kSteps];
+  h8 qreg[kQueriesInLds ? 1 : NQ][kSteps];
   float f[NQ], m[NQ], l[NQ];
   f4 o[NQ][kBlocks];
-#pragma unroll
-  for (int n = 0; n < NQ; ++n) {
+  // one tile's fragments as a wavefront's lanes hold them, and its factor
+  auto load_queries = [&](int n, h8 (&q)[kSteps]) {
     const int r = n * 16 + i;
     const int qi = (row0 + r) / a.group, hh = (row0 + r) - qi * a.group;
     const bool live = r < nrows;
-    pos[n] = s.len - s.ql + qi;
-    f[n] = a.f;
-    m[n] = kNoToken;
-    l[n] = 0.f;
-#pragma unroll
-    for (int j = 0; j < kBlocks; ++j) o[n][j] = f4{0.f, 0.f, 0.f, 0.f};
     const int64_t at = static_cast<int64_t>(s.qs + (live ? qi : 0)) * a.q_ts +
                        static_cast<int64_t>(head * a.group + (live ? hh : 0)) * a.q_hs + g * (DIM / 4);
     uint16_t raw[DIM / 4];
@@ -315,6 +356,7 @@ __global__ __launch_bounds__(kW * 64) void kv4_attention_kernel(const AttnParams
 #pragma unroll
       for (int e = 0; e < DIM / 4; ++e) raw[e] = src[e];
     }
+    float factor = a.f;
     if constexpr (BF16) {
       // a power of two that brings the row's largest magnitude to [1, 2)
       uint32_t top = 0;
@@ -325,17 +367,47 @@ __global__ __launch_bounds__(kW * 64) void kv4_attention_kernel(const AttnParams
       // (a row below 2^-60 by 2^60; inf and NaN stay themselves)
       const int e2 = min(max(static_cast<int>(top >> 7), 67), 252) - 127;
       const float down = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
-      f[n] = a.f * __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
+      factor = a.f * __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
 #pragma unroll
       for (int e = 0; e < DIM / 4; ++e) {
         const float x = __uint_as_float(static_cast<uint32_t>(raw[e]) << 16);
-        q[n][e / 8][e % 8] = live ? static_cast<_Float16>(x * down) : static_cast<_Float16>(0.f);
+        q[e / 8][e % 8] = live ? static_cast<_Float16>(x * down) : static_cast<_Float16>(0.f);
       }
     } else {
 #pragma unroll
       for (int e = 0; e < DIM / 4; ++e)
-        q[n][e / 8][e % 8] = live ? __builtin_bit_cast(_Float16, raw[e]) : static_cast<_Float16>(0.f);
+        q[e / 8][e % 8] = live ? __builtin_bit_cast(_Float16, raw[e]) : static_cast<_Float16>(0.f);
     }
+    return factor;
+  };
+  if constexpr (kQueriesInLds) {
+    for (int n = wave; n < NQ; n += kW) {
+      h8 q[kSteps];
+      const float factor = load_queries(n, q);
+#pragma unroll
+      for (int c = 0; c < kSteps; ++c) sh.q[(n * kSteps + c) * 64 + lane] = __builtin_bit_cast(u4, q[c]);
+      if (g == 0) fs[n * 16 + i] = factor;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) f[n] = fs[n * 16 + i];
+  } else {
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) f[n] = load_queries(n, qreg[n]);
+  }
+  const auto query = [&](int n, int c) -> h8 {
+    if constexpr (kQueriesInLds)
+      return __builtin_bit_cast(h8, sh.q[(n * kSteps + c) * 64 + lane]);
+    else
+      return qreg[n][c];
+  };
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    pos[n] = s.len - s.ql + (row0 + n * 16 + i) / a.group;
+    m[n] = kNoToken;
+    l[n] = 0.f;
+#pragma unroll
+    for (int j = 0; j < kBlocks; ++j) o[n][j] = f4{0.f, 0.f, 0.f, 0.f};
   }
 
   // The unit's tiles, cut to what this row tile's rows see at all.
@@ -361,49 +433,82 @@ __global__ __launch_bounds__(kW * 64) void kv4_attention_kernel(const AttnParams
       pid[h] = p >= 0 && p < a.pages ? p : -1;
     }
   };
-  auto load = [&](Tile<DIM>& t, int (&pg)[2], int j) {
-    if ((j & 63) == 0) pages_from(j);
-    const int tok = (t0 + wave + j * kW) * kTileTokens;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      pg[h] = __builtin_amdgcn_readlane(pid[h], j & 63);
-      const uint8_t* seg = head_base + static_cast<int64_t>(max(pg[h], 0)) * a.page_bytes;
-      load_half<DIM>(t, h, seg, (tok + 16 * h) & (page - 1), page, lane);
-    }
+  // Keys and values of tile j, the pages having been looked up.
+  Tile<DIM> t;
+  int pg[2] = {-1, -1};   // the pages of the tile in hand
+  const auto token_of = [&](int j) { return (t0 + wave + j * kW) * kTileTokens; };
+  const auto segment = [&](int p) {
+    return segment_of(head_base + static_cast<int64_t>(max(p, 0)) * a.page_bytes, a.seg_bytes);
   };
-  auto compute = [&](const Tile<DIM>& t, const int (&pg)[2], int j) {
-    const int tok = (t0 + wave + j * kW) * kTileTokens;
+  auto look_up = [&](int (&next)[2], int j) {
+    if ((j & 63) == 0) pages_from(j);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) next[h] = __builtin_amdgcn_readlane(pid[h], j & 63);
+  };
+  auto keys = [&](const int (&p)[2], int j) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      load_keys<DIM>(t, h, segment(p[h]), (token_of(j) + 16 * h) & (page - 1), page, lane);
+  };
+  auto vals = [&](const int (&p)[2], int j) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      load_vals<DIM>(t, h, segment(p[h]), (token_of(j) + 16 * h) & (page - 1), page, lane);
+  };
+  if (mine > 0) {
+    look_up(pg, 0);
+    keys(pg, 0);
+    vals(pg, 0);
+  }
+  // The keys of the next tile are on their way during this one's softmax and
+  // values, its values during the next one's scores: one set of registers
+  // each, and the other wavefronts of the SIMD to fill what is left.
+  for (int j = 0; j < mine; ++j) {
+    const int tok = token_of(j);
     f4 sc[2][NQ];
-    scores<DIM, NQ>(t, 0, q, sc[0]);
-    scores<DIM, NQ>(t, 1, q, sc[1]);
+    scores<DIM, NQ>(t, query, sc);
+    __builtin_amdgcn_sched_barrier(0);
+    int next[2] = {-1, -1};
+    if (j + 1 < mine) {
+      look_up(next, j + 1);
+      keys(next, j + 1);
+    }
+    __builtin_amdgcn_sched_barrier(0);
     uint32_t vs[2] = {t.vs[0], t.vs[1]};
-    const bool whole = tok + kTileTokens - 1 <= first_pos && (win == 0 || tok > last_pos - win) && pg[0] >= 0 && pg[1] >= 0;
+    const bool whole =
+        tok + kTileTokens - 1 <= first_pos && (win == 0 || tok > last_pos - win) && pg[0] >= 0 && pg[1] >= 0;
     if (!whole) {
       // Scores of unseen tokens become -inf whatever the cache holds there,
       // and the values of tokens past the end or of absent pages are zeroed:
-      // such bytes may decode to NaN, which a p of 0 would not remove.
+      // such bytes may decode to NaN, which a p of 0 would not remove. Bit b
+      // of a mask stands for token tok + 4 g + b.
+      const int at = tok + 4 * g;
+      const auto up_to = [](int x) -> uint32_t { return x < 0 ? 0u : x >= 31 ? ~0u : (2u << x) - 1u; };
+      const uint32_t held = up_to(s.len - 1 - at) & ((pg[0] >= 0 ? 0xFFFFu : 0u) | (pg[1] >= 0 ? 0xFFFF0000u : 0u));
+      const auto bit = [](uint32_t w, int b) { return static_cast<uint32_t>(static_cast<int32_t>(w << (31 - b)) >> 31); };
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int th = tok + 16 * h + g * 4;
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const bool held = th + e < s.len && pg[h] >= 0;
-          if (!held) vs[h] &= ~(0xFFu << (8 * e));
+        for (int e = 0; e < 4; ++e) vs[h] &= ~(0xFFu << (8 * e)) | bit(held, 16 * h + e);
 #pragma unroll
-          for (int n = 0; n < NQ; ++n) {
-            const bool seen = held && th + e <= pos[n] && (win == 0 || th + e > pos[n] - win);
-            if (!seen) sc[h][n][e] = -__builtin_inff();
+      for (int n = 0; n < NQ; ++n) {
+        const uint32_t seen = held & up_to(pos[n] - at) & (win ? ~up_to(pos[n] - win - at) : ~0u);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t k = bit(seen, 16 * h + e);
+            sc[h][n][e] = __uint_as_float((__float_as_uint(sc[h][n][e]) & k) | (0xFF800000u & ~k));
           }
-        }
       }
     }
     float far = -__builtin_inff();
     float top[NQ];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      top[n] = fmaxf(fmaxf(fmaxf(sc[0][n][0], sc[0][n][1]), fmaxf(sc[0][n][2], sc[0][n][3])),
-                     fmaxf(fmaxf(sc[1][n][0], sc[1][n][1]), fmaxf(sc[1][n][2], sc[1][n][3])));
-      far = fmaxf(far, fmaf(top[n], f[n], -m[n]));
+      top[n] = max3(max3(sc[0][n][0], sc[0][n][1], sc[0][n][2]), sc[0][n][3], sc[1][n][0]);
+      top[n] = max2(max3(top[n], sc[1][n][1], sc[1][n][2]), sc[1][n][3]);
+      far = max2(far, fmaf(top[n], f[n], -m[n]));
     }
     if (__any(far > kHeadroom)) {
 #pragma unroll
@@ -420,27 +525,20 @@ __global__ __launch_bounds__(kW * 64) void kv4_attention_kernel(const AttnParams
     }
     h8 p[NQ];
 #pragma unroll
-    for (int n = 0; n < NQ; ++n)
+    for (int n = 0; n < NQ; ++n) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
+        // (the sum takes p before it is rounded: lse keeps its 32 bits)
         const float x = __builtin_amdgcn_exp2f(fmaf(sc[e / 4][n][e % 4], f[n], -m[n]));
         l[n] += x;
         p[n][e] = static_cast<_Float16>(x);
       }
+    }
     values<DIM, NQ>(t, vs, p, o);
-  };
-
-  Tile<DIM> ta, tb;
-  int pa[2], pb[2];
-  if (mine > 0) load(ta, pa, 0);
-  for (int j = 0; j < mine; j += 2) {
-    if (j + 1 < mine) load(tb, pb, j + 1);
     __builtin_amdgcn_sched_barrier(0);
-    compute(ta, pa, j);
-    if (j + 1 >= mine) break;
-    if (j + 2 < mine) load(ta, pa, j + 2);
+    if (j + 1 < mine) vals(next, j + 1);
     __builtin_amdgcn_sched_barrier(0);
-    compute(tb, pb, j + 1);
+    pg[0] = next[0], pg[1] = next[1];
   }
 
   // Join the wavefronts: a row's reference becomes the largest of the four.
@@ -596,10 +694,10 @@ hipError_t launch_nq(int nq, const AttnParams& a, hipStream_t stream) {
     case 2: return launch_as<DIM, 2, BF16>(a, stream);
     default: break;
   }
-  if constexpr (DIM != 256) {
+  if constexpr (DIM != 256)
     if (nq == 3) return launch_as<DIM, 3, BF16>(a, stream);
+  if constexpr (DIM == 64)
     if (nq == 4) return launch_as<DIM, 4, BF16>(a, stream);
-  }
   return hipErrorInvalidValue;
 }
 

@@ -17,6 +17,9 @@ constexpr int64_t kMaxStride = int64_t(1) << 40;  // elements; keeps every 64-bi
 
 constexpr int64_t kMaxGroups = int64_t(1) << 23;  // workgroups of a launch: 2^31 threads
 
+// Sequences of at most this many tokens are not cut.
+constexpr int kWholeRunTokens = 512;
+
 bool positive(float x) { return isfinite(x) && x > 0.0f; }
 
 bool page_size_ok(int32_t p) { return p == 16 || p == 32 || p == 64 || p == 128 || p == 256; }
@@ -97,14 +100,16 @@ qpn_status plan_attention(const qpn_kv4_cache* c, const qpn_kv4_attention_args* 
   p->row_tiles = static_cast<int>((t16 + most - 1) / most);
   p->tiles16 = static_cast<int>((t16 + p->row_tiles - 1) / p->row_tiles);
   p->row_tiles = static_cast<int>((t16 + p->tiles16 - 1) / p->tiles16);
-  p->slots = 512;
-  p->min_chunk = kAttnWaves;
-  p->max_units = p->slots + static_cast<int64_t>(a->batch) * p->row_tiles * c->kv_heads;
-  if (p->max_units > kMaxGroups || static_cast<int64_t>(a->rows) * a->heads > kMaxGroups) return QPN_ERR_UNSUPPORTED;
-  p->sched_bytes = round16(static_cast<size_t>(a->batch) * 16);
-  const size_t r = static_cast<size_t>(16) * p->tiles16;
-  p->partial_bytes = r * (static_cast<size_t>(c->head_dim) + 2) * sizeof(float);
-  p->total_bytes = a->batch == 0 || a->rows == 0 ? 0 : p->sched_bytes + p->partial_bytes * p->max_units;
+  // the tiles of all sequences, row tiles and heads are counted in 32 bits
+  const int64_t runs = static_cast<int64_t>(a->batch) * p->row_tiles * c->kv_heads;
+  const int64_t tiles = std::max<int64_t>(1, (static_cast<int64_t>(a->max_kv_len) + kTileTokens - 1) / kTileTokens) + 64;
+  if (runs > kMaxGroups || runs * tiles > INT32_MAX - (1 << 20)) return QPN_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(a->rows) * a->heads > kMaxGroups) return QPN_ERR_UNSUPPORTED;
+  p->groups = a->max_kv_len <= kWholeRunTokens ? 0 : kComputeUnits * attn_waves_per_simd(c->head_dim, p->tiles16);
+  p->min_share = kAttnWaves;
+  p->sched_bytes = (static_cast<size_t>(a->batch) + 1) * 16;
+  p->partial_bytes = 2 * static_cast<size_t>(p->groups) * 16 * p->tiles16 * (c->head_dim + 2) * sizeof(float);
+  p->total_bytes = a->batch == 0 || a->rows == 0 || p->groups == 0 ? 0 : p->sched_bytes + p->partial_bytes;
   return QPN_OK;
 }
 

@@ -6,18 +6,25 @@
 
 namespace qpn {
 
-// The shape of an attention launch, chosen by plan_attention.
-struct AttentionPlan {
-  int tiles16;        // 16-row query tiles a wavefront holds (template NQ)
-  int row_tiles;      // workgroups that share a sequence's rows, at most
-  int slots;          // workgroups that the tokens are spread over
-  int min_chunk;      // 32-token tiles a workgroup takes at least
-  int64_t max_units;  // workgroups launched, and partials held
-  size_t sched_bytes, partial_bytes, total_bytes;
-};
-
 constexpr int kAttnWaves = 4;   // wavefronts a workgroup
 constexpr int kTileTokens = 32; // tokens a wavefront takes at a time
+constexpr int kComputeUnits = 256;
+
+// Wavefronts of the attention kernel that a SIMD holds, with nq 16-row tiles
+// each: 512 / waves registers hold the output (nq * dim / 4 of them) and what
+// a step needs; heads of 256 are kept to 2 by their LDS.
+constexpr int attn_waves_per_simd(int dim, int nq) {
+  return dim == 256 || nq >= (dim == 64 ? 4 : 3) ? 2 : nq * dim <= 128 ? 4 : 3;
+}
+
+// The shape of an attention launch, chosen by plan_attention.
+struct AttentionPlan {
+  int tiles16;    // 16-row query tiles a wavefront holds (template NQ)
+  int row_tiles;  // a sequence's row tiles, at most
+  int groups;     // workgroups that share the tiles evenly; 0: a workgroup a run, no join
+  int min_share;  // tiles a workgroup takes at least
+  size_t sched_bytes, partial_bytes, total_bytes;
+};
 
 int64_t kv4_segment_bytes(int page_size, int head_dim);
 qpn_status check_kv4_cache(const qpn_kv4_cache* c);

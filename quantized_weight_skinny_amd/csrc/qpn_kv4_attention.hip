@@ -34,6 +34,9 @@ namespace {
 constexpr int kW = kAttnWaves;
 constexpr float kNoToken = -1e30f;  // a row's reference before it has seen a token
 constexpr float kBias = 8.0f, kHeadroom = 15.0f;
+// What a run costs besides its tiles, in tiles: its queries, the first loads'
+// latency and the joining of the wavefronts.
+constexpr int kRunCost = 20;
 
 struct AttnParams {
   const uint8_t* cache;  // the layer
@@ -47,11 +50,10 @@ struct AttnParams {
   int64_t table_stride;
   const int32_t* kv_len;
   const int32_t* q_start;
-  int32_t batch, rows, max_q, max_kv, window, slots, min_chunk, q_aligned;
-  int64_t max_units;
+  int32_t batch, rows, max_q, max_kv, window, row_tiles, groups, min_share, q_aligned;
   float f, v_scale;  // f: scale * log2(e) * k_scale
-  int4* sched;       // [batch]: first unit, splits, row tiles, -
-  float* part;       // [unit][16 NQ][DIM], then [unit][16 NQ][2]
+  int4* sched;       // [batch]: where the sequence's tiles begin, their number, row tiles; then [1]: the share
+  float* part;       // [2 groups][16 NQ][DIM], then [2 groups][16 NQ][2]; groups 0: no join
 };
 
 // One sequence's share of the work.
@@ -72,15 +74,9 @@ __device__ __forceinline__ Seq sequence(const AttnParams& a, int b, int rows_per
   // the first token that the sequence's first row sees
   const int first = a.window ? max(0, s.len - s.ql - a.window + 1) : 0;
   s.lo = first / kTileTokens;
-  s.tiles = (s.len + kTileTokens - 1) / kTileTokens - s.lo;
+  s.tiles = max(1, (s.len + kTileTokens - 1) / kTileTokens - s.lo);  // an empty sequence is one tile that holds nothing
   s.rt = (s.ql * a.group + rows_per_tile - 1) / rows_per_tile;
   return s;
-}
-
-__device__ __forceinline__ long long wave_sum(long long v) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o);
-  return v;
 }
 
 // The codes and scales of 32 tokens as a lane holds them.
@@ -113,27 +109,38 @@ __device__ __forceinline__ void load_words(uint32_t (&r)[WORDS], __amdgpu_buffer
   }
 }
 
-// Half `h` (16 tokens from offset `off` of a page's segment `seg`): the keys,
-// and the values.
+// A lane's byte offsets in a segment's four arrays.
 template <int DIM>
-__device__ __forceinline__ void load_keys(Tile<DIM>& t, int h, __amdgpu_buffer_rsrc_t seg, int off, int page, int lane) {
-  const int i = lane & 15, g = lane >> 4;
-  load_words(t.k[h], seg, i * (DIM / 2) + g * (DIM / 8), off * (DIM / 2));
-  const int lane_at = i * (DIM / 16) + g * (DIM / 64), at = page * DIM + off * (DIM / 16);
+struct LaneOffsets {
+  int k, v, ks, vs;
+  __device__ __forceinline__ LaneOffsets(int lane, int page) {
+    const int i = lane & 15, g = lane >> 4;
+    k = i * (DIM / 2) + g * (DIM / 8);
+    v = page * (DIM / 2) + lane_v<DIM>(i, g);
+    ks = page * DIM + i * (DIM / 16) + g * (DIM / 64);
+    vs = page * DIM + page * (DIM / 16) + g * (DIM / 4) + (i * DIM / 256) * 4;
+  }
+};
+
+// Half `h` (16 tokens), whose codes begin `codes` and whose scales begin
+// `scales` bytes into their arrays: the keys, and the values.
+template <int DIM>
+__device__ __forceinline__ void load_keys(Tile<DIM>& t, int h, __amdgpu_buffer_rsrc_t seg, const LaneOffsets<DIM>& at,
+                                          int codes, int scales) {
+  load_words(t.k[h], seg, at.k, codes);
   if constexpr (DIM == 64)
-    t.ks[h] = __builtin_amdgcn_raw_buffer_load_b8(seg, lane_at, at, Stream::kStreaming);
+    t.ks[h] = __builtin_amdgcn_raw_buffer_load_b8(seg, at.ks, scales, Stream::kStreaming);
   else if constexpr (DIM == 128)
-    t.ks[h] = __builtin_amdgcn_raw_buffer_load_b16(seg, lane_at, at, Stream::kStreaming);
+    t.ks[h] = __builtin_amdgcn_raw_buffer_load_b16(seg, at.ks, scales, Stream::kStreaming);
   else
-    t.ks[h] = __builtin_amdgcn_raw_buffer_load_b32(seg, lane_at, at, Stream::kStreaming);
+    t.ks[h] = __builtin_amdgcn_raw_buffer_load_b32(seg, at.ks, scales, Stream::kStreaming);
 }
 
 template <int DIM>
-__device__ __forceinline__ void load_vals(Tile<DIM>& t, int h, __amdgpu_buffer_rsrc_t seg, int off, int page, int lane) {
-  const int i = lane & 15, g = lane >> 4;
-  load_words(t.v[h], seg, lane_v<DIM>(i, g), page * (DIM / 2) + off * (DIM / 2));
-  t.vs[h] = __builtin_amdgcn_raw_buffer_load_b32(seg, g * (DIM / 4) + (i * DIM / 256) * 4,
-                                                 page * DIM + page * (DIM / 16) + off * (DIM / 16), Stream::kStreaming);
+__device__ __forceinline__ void load_vals(Tile<DIM>& t, int h, __amdgpu_buffer_rsrc_t seg, const LaneOffsets<DIM>& at,
+                                          int codes, int scales) {
+  load_words(t.v[h], seg, at.v, codes);
+  t.vs[h] = __builtin_amdgcn_raw_buffer_load_b32(seg, at.vs, scales, Stream::kStreaming);
 }
 
 // The larger of three (two). The compiler's fmaxf first quiets each operand
@@ -251,21 +258,28 @@ __device__ __forceinline__ void store_out8(void* out, int64_t at, const float (&
   *reinterpret_cast<u4*>(static_cast<uint16_t*>(out) + at) = w;
 }
 
-// Wavefronts a SIMD is to hold: the output tiles and what a step needs fit
-// 512 / waves registers (NQ * DIM / 4 of them for the output).
-constexpr int waves_per_simd(int dim, int nq) {
-  return dim == 256 || nq >= (dim == 64 ? 4 : 3) ? 2 : nq * dim <= 128 ? 4 : 3;
+// The kernel's arguments, to be read again from where they lie.
+typedef const AttnParams __attribute__((address_space(4))) * ParamsPtr;
+__device__ __forceinline__ const AttnParams& reread(const AttnParams&) {
+  ParamsPtr p = (ParamsPtr)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const AttnParams*)p;
 }
 
-// Workgroup u takes unit u: of one sequence, a run of tiles, a row tile and a
-// kv head. The units are counted out on the device from the lengths, so a
-// captured call follows them: with `total` tiles to do over all sequences, row
-// tiles and heads, a unit is max(min_chunk, ceil(total / slots)) tiles, and
-// every sequence is cut into whole units. Heads run fastest (neighbouring
-// workgroups read neighbouring segments of one page), then row tiles: with 8
-// heads or a multiple, the row tiles that read the same tokens land on the same XCD.
+// The work is the tiles of all (sequence, row tile, kv head), laid end to end
+// in that order. Where a sequence may be long, each of `groups` workgroups (as
+// many as the device holds at once) takes an equal share of that line, at
+// least min_share tiles, whatever the lengths: a share may begin inside one
+// run of tiles and end inside another. A run that lies in one share is
+// written as it is; the pieces of any other go to the workspace, at most two a
+// workgroup (the end of a run in slot 2 w, the beginning of one in slot
+// 2 w + 1), and the join kernel adds them. The line is measured out on the
+// device from the lengths, so a captured call follows them. Where every
+// sequence is short (groups 0), a workgroup takes a run, and no length but its
+// own matters.
 template <int DIM, int NQ, bool BF16>
-__global__ __launch_bounds__(kW * 64, waves_per_simd(DIM, NQ)) void kv4_attention_kernel(const AttnParams a) {
+__global__ __launch_bounds__(kW * 64, attn_waves_per_simd(DIM, NQ)) void kv4_attention_kernel(const AttnParams params) {
+
   constexpr int kRows = 16 * NQ, kBlocks = DIM / 16, kSteps = DIM / 32;
   constexpr int kPad = DIM + 4;
   constexpr bool kQueriesInLds = NQ * DIM > 128;
@@ -277,123 +291,262 @@ __global__ __launch_bounds__(kW * 64, waves_per_simd(DIM, NQ)) void kv4_attentio
   __shared__ float2 ml[kW][kRows];
   __shared__ float fs[kRows];
   auto& red = sh.red;
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int i = lane & 15, g = lane >> 4;
-  const int unit = blockIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+  int tid = threadIdx.x, lane = tid & 63;
+  const int group_id = blockIdx.x;
 
-  // Which sequence, and how long a unit is.
-  long long total = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += 64) {
-    const int b = b0 + lane;
-    if (b < a.batch) {
-      const Seq s = sequence(a, b, kRows);
-      total += static_cast<long long>(max(s.tiles, 1)) * s.rt;
-    }
-  }
-  total = wave_sum(total) * a.kv_heads;
-  // no sequence is longer than 2^30 tokens: a chunk that is cut there holds any
-  // (the same in every lane: held in a scalar register, like all that follows from it)
-  const int chunk = __builtin_amdgcn_readfirstlane(
-      max(a.min_chunk, static_cast<int>(min((total + a.slots - 1) / a.slots, 1ll << 26))));
-  int b = -1, base = 0, splits = 0;
-  for (int b0 = 0, before = 0; b0 < a.batch; b0 += 64) {
-    const int bl = b0 + lane;
-    int n = 0, units = 0;
-    if (bl < a.batch) {
-      const Seq s = sequence(a, bl, kRows);
-      n = max(1, (s.tiles + chunk - 1) / chunk);
-      units = n * s.rt * a.kv_heads;
-    }
-    int sum = units;  // inclusive running sum over the lanes
+  const AttnParams& a0 = params;
+  // This workgroup's share [at, end) of the line, and the sequence b, whose
+  // tiles begin at `base`, that the share begins in.
+  int b = 0, base = 0, at, end;
+  if (a0.groups == 0) {
+    const int per = a0.row_tiles * a0.kv_heads;
+    b = group_id / per;
+    const Seq s = sequence(a0, b, kRows);
+
+    at = (group_id - b * per) * (s.tiles + kRunCost);
+    end = at + s.tiles + kRunCost;
+    if (at >= s.rt * a0.kv_heads * (s.tiles + kRunCost)) return;  // the sequence has fewer row tiles than the longest
+  } else {
+    int total = 0;
+    int mine = 0, sum = 0;  // of the last 64 sequences: a lane's tiles, and their running sum
+    const auto count = [&](int b0) {
+      mine = 0;
+      if (b0 + lane < a0.batch) {
+        const Seq s = sequence(a0, b0 + lane, kRows);
+        mine = (s.tiles + kRunCost) * s.rt * a0.kv_heads;
+      }
+      sum = mine;
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int x = __shfl_up(sum, o);
-      if (lane >= o) sum += x;
+      for (int o = 1; o < 64; o <<= 1) {
+        const int x = __shfl_up(sum, o);
+        if (lane >= o) sum += x;
+      }
+    };
+    for (int b0 = 0; b0 < a0.batch; b0 += 64) {
+      count(b0);
+      total += __builtin_amdgcn_readlane(sum, 63);
     }
-    const int first = before + sum - units;
-    const unsigned long long hit = __ballot(unit >= first && unit < first + units);
-    if (hit) {
-      const int l = __builtin_ctzll(hit);
-      b = b0 + l;
-      base = __builtin_amdgcn_readlane(first, l);
-      splits = __builtin_amdgcn_readlane(n, l);
-      break;
+    const int share = max(a0.min_share, (total + a0.groups - 1) / a0.groups);
+    if (group_id == 0 && tid == 0) a0.sched[a0.batch] = int4{share, 0, 0, 0};
+    at = group_id * share;  // groups * share is at most 2^31 - 1, as the line is
+    end = min(at + share, total);
+    if (at >= total) return;
+    int before = 0;
+
+    for (int b0 = 0; b0 < a0.batch; b0 += 64) {
+      if (a0.batch > 64) count(b0);
+      const int all = __builtin_amdgcn_readlane(sum, 63);
+      if (at < before + all) {
+        const int l = __builtin_ctzll(__ballot(at < before + sum));
+        b = b0 + l;
+        base = before + __builtin_amdgcn_readlane(sum, l) - __builtin_amdgcn_readlane(mine, l);
+        break;
+      }
+      before += all;
     }
-    before += __builtin_amdgcn_readlane(sum, 63);
   }
-  if (b < 0) return;  // the grid is the largest number of units
-  b = __builtin_amdgcn_readfirstlane(b);
+  while (true) {
+  // (what follows from the lane is worked out again for every run: kept from
+  // one to the next it would take registers that the occupancy needs;
+  // and so are the arguments, which come from the scalar cache)
+  asm volatile("" : "+v"(tid), "+v"(lane));
+  const AttnParams& a = reread(params);
+  const int i = lane & 15, g = lane >> 4;
   const Seq s = sequence(a, b, kRows);
-  int rest = unit - base;
-  const int head = rest % a.kv_heads;
-  rest /= a.kv_heads;
-  const int rtile = rest % s.rt, split = rest / s.rt;
-  if (rest == 0 && head == 0 && tid == 0) a.sched[b] = int4{base, splits, s.rt, 0};
+  const int cost = s.tiles + kRunCost;
+  const int run = (at - base) / cost, from = at - base - run * cost, to = min(cost, from + end - at);
+  const int tile0 = max(0, from - kRunCost), tiles = max(0, to - kRunCost) - tile0;
+  at += to - from;
+  const int rtile = run / a.kv_heads, head = run - rtile * a.kv_heads;
+  const bool alone = tiles == s.tiles;  // the whole run
+  if (a.groups && run == 0 && from == 0 && tid == 0) a.sched[b] = int4{base, s.tiles, 0, 0};
+  if (tiles > 0) {
 
   // The rows: row r of the row tile is query row r / group, head r % group.
   const int row0 = rtile * kRows, nrows = min(s.ql * a.group - row0, kRows);
-  int pos[NQ];
   h8 qreg[kQueriesInLds ? 1 : NQ][kSteps];
   float f[NQ], m[NQ], l[NQ];
   f4 o[NQ][kBlocks];
-  // one tile's fragments as a wavefront's lanes hold them, and its factor
-  auto load_queries = [&](int n, h8 (&q)[kSteps]) {
+  // Row tile n's queries as a wavefront's lanes hold them: a lane's part of its
+  // row in memory, eight elements of it as they lie there, and as a fragment.
+  const auto row_of = [&](int n) {
     const int r = n * 16 + i;
     const int qi = (row0 + r) / a.group, hh = (row0 + r) - qi * a.group;
-    const bool live = r < nrows;
-    const int64_t at = static_cast<int64_t>(s.qs + (live ? qi : 0)) * a.q_ts +
-                       static_cast<int64_t>(head * a.group + (live ? hh : 0)) * a.q_hs + g * (DIM / 4);
-    uint16_t raw[DIM / 4];
-    const uint16_t* src = static_cast<const uint16_t*>(a.q) + at;
+    const bool live = r < nrows;  // (a row past the last loads the first)
+    const int64_t row_at = static_cast<int64_t>(s.qs + (live ? qi : 0)) * a.q_ts +
+                           static_cast<int64_t>(head * a.group + (live ? hh : 0)) * a.q_hs + g * (DIM / 4);
+    return static_cast<const uint16_t*>(a.q) + row_at;
+  };
+  const auto eight = [&](const uint16_t* src, int c) {
+    u4 x;
     if (a.q_aligned) {
-#pragma unroll
-      for (int c = 0; c < kSteps; ++c) {
-        const u4 x = *reinterpret_cast<const u4*>(src + c * 8);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) raw[c * 8 + e] = static_cast<uint16_t>(x[e / 2] >> (16 * (e & 1)));
-      }
+      x = *reinterpret_cast<const u4*>(src + c * 8);
     } else {
 #pragma unroll
-      for (int e = 0; e < DIM / 4; ++e) raw[e] = src[e];
+      for (int e = 0; e < 4; ++e) x[e] = src[c * 8 + 2 * e] | static_cast<uint32_t>(src[c * 8 + 2 * e + 1]) << 16;
     }
-    float factor = a.f;
+    return x;
+  };
+  // bf16: the exponent (clamped: a row below 2^-60 by 2^60; inf and NaN stay
+  // themselves) that brings a row's largest magnitude to [1, 2).
+  const auto larger = [](uint32_t top, const u4& x) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) top = max(max(top, x[e] & 0x7FFFu), (x[e] >> 16) & 0x7FFFu);
+    return top;
+  };
+  const auto exponent = [](uint32_t top) {
+    top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16)));
+    top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32)));
+    return min(max(static_cast<int>(top >> 7), 67), 252) - 127;
+  };
+  const auto fragment = [&](int n, u4 x, int e2) {
+    if (n * 16 + i >= nrows) x = u4{0u, 0u, 0u, 0u};
     if constexpr (BF16) {
-      // a power of two that brings the row's largest magnitude to [1, 2)
-      uint32_t top = 0;
-#pragma unroll
-      for (int e = 0; e < DIM / 4; ++e) top = max(top, static_cast<uint32_t>(raw[e]) & 0x7FFFu);
-      top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16)));
-      top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32)));
-      // (a row below 2^-60 by 2^60; inf and NaN stay themselves)
-      const int e2 = min(max(static_cast<int>(top >> 7), 67), 252) - 127;
       const float down = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
-      factor = a.f * __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
+      h8 q;
 #pragma unroll
-      for (int e = 0; e < DIM / 4; ++e) {
-        const float x = __uint_as_float(static_cast<uint32_t>(raw[e]) << 16);
-        q[e / 8][e % 8] = live ? static_cast<_Float16>(x * down) : static_cast<_Float16>(0.f);
+      for (int e = 0; e < 4; ++e) {
+        q[2 * e] = static_cast<_Float16>(__uint_as_float(x[e] << 16) * down);
+        q[2 * e + 1] = static_cast<_Float16>(__uint_as_float(x[e] & 0xFFFF0000u) * down);
       }
+      return q;
     } else {
-#pragma unroll
-      for (int e = 0; e < DIM / 4; ++e)
-        q[e / 8][e % 8] = live ? __builtin_bit_cast(_Float16, raw[e]) : static_cast<_Float16>(0.f);
+      return __builtin_bit_cast(h8, x);
     }
-    return factor;
+  };
+  const auto factor = [&](int e2) {
+    return BF16 ? a.f * __uint_as_float(static_cast<uint32_t>(127 + e2) << 23) : a.f;
+  };
+  // They are asked for before the first keys and values and made into
+  // fragments while those come; in LDS, wavefront n does tile n for all four.
+  // Two tiles of 256 would have too many registers on the way: those queries
+  // come first, eight elements at a time, bf16 rows twice.
+  static_assert(NQ <= kW, "a wavefront prepares one tile");
+  constexpr bool kQueriesFirst = NQ * DIM == 512;
+  u4 raw[kQueriesFirst ? 1 : kQueriesInLds ? 1 : NQ][kQueriesFirst ? 1 : kSteps];
+  if constexpr (kQueriesFirst) {
+    if (wave < NQ) {
+      const uint16_t* src = row_of(wave);
+      int e2 = 0;
+      if constexpr (BF16) {
+        uint32_t top = 0;
+#pragma unroll 1
+        for (int c = 0; c < kSteps; ++c) top = larger(top, eight(src, c));
+        e2 = exponent(top);
+      }
+#pragma unroll 1
+      for (int c = 0; c < kSteps; ++c)
+        sh.q[(wave * kSteps + c) * 64 + lane] = __builtin_bit_cast(u4, fragment(wave, eight(src, c), e2));
+      if (g == 0) fs[wave * 16 + i] = factor(e2);
+    }
+  } else if constexpr (kQueriesInLds) {
+    if (wave < NQ) {
+      const uint16_t* src = row_of(wave);
+#pragma unroll
+      for (int c = 0; c < kSteps; ++c) raw[0][c] = eight(src, c);
+    }
+  } else {
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      const uint16_t* src = row_of(n);
+#pragma unroll
+      for (int c = 0; c < kSteps; ++c) raw[n][c] = eight(src, c);
+    }
+  }
+
+  // The tiles in hand, cut to what this row tile's rows see at all.
+  const int first_pos = s.len - s.ql + row0 / a.group, last_pos = s.len - s.ql + (row0 + nrows - 1) / a.group;
+  const int win = a.window;
+  int t0 = s.lo + tile0, t1 = t0 + tiles;
+  t1 = min(t1, last_pos / kTileTokens + (last_pos >= 0));
+  if (win) t0 = max(t0, max(0, first_pos - win + 1) / kTileTokens);
+  const int mine = t1 > t0 + wave && a.pages > 0 ? (t1 - t0 - wave + kW - 1) / kW : 0;  // this wavefront's tiles
+  const int page = 1 << a.page_shift;
+  const int32_t* table = a.table + static_cast<int64_t>(b) * a.table_stride;
+  const uint8_t* head_base = a.cache + static_cast<int64_t>(head) * a.seg_bytes;
+
+  // The page segments of the wavefront's next 64 tiles, a lane each, and which
+  // of their halves have none. A half's loads take their base from here and
+  // their place in the page from the token, in scalar registers throughout.
+  uint64_t base_of[2], absent[2] = {0, 0};
+  auto pages_from = [&](int j0) {
+    const int j = j0 + lane;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int tok = (t0 + wave + j * kW) * kTileTokens + 16 * h;
+      int p = -1;
+      if (j < mine && tok < s.len) p = table[tok >> a.page_shift];
+      const bool none = p < 0 || p >= a.pages;
+      base_of[h] = reinterpret_cast<uint64_t>(head_base) + static_cast<uint64_t>(none ? 0 : p) * a.page_bytes;
+      absent[h] = __ballot(none);
+    }
+  };
+  // Tile j's place: the segments of its halves and their tokens' offsets in
+  // the codes and in the scales. Past the last tile the segments are empty:
+  // loads there bring zeros and no traffic, and as every step has the same
+  // loads, a wait for the older ones need not be a wait for all.
+  struct Place {
+    __amdgpu_buffer_rsrc_t seg[2];
+    int codes[2], scales[2];
+  };
+  const auto place = [&](int j) {
+    Place r;
+    if ((j & 63) == 0) pages_from(j);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(base_of[h]), j & 63);
+      const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(base_of[h] >> 32), j & 63);
+      r.seg[h] = segment_of(reinterpret_cast<const uint8_t*>(static_cast<uint64_t>(hi) << 32 | lo),
+                            j < mine ? a.seg_bytes : 0);
+      const int off = ((t0 + wave + j * kW) * kTileTokens + 16 * h) & (page - 1);
+      r.codes[h] = off * (DIM / 2);
+      r.scales[h] = off * (DIM / 16);
+    }
+    return r;
+  };
+  Tile<DIM> t;
+  const LaneOffsets<DIM> lane_at(lane, page);
+  if (mine > 0) {
+    const Place r = place(0);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) load_keys<DIM>(t, h, r.seg[h], lane_at, r.codes[h], r.scales[h]);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) load_vals<DIM>(t, h, r.seg[h], lane_at, r.codes[h], r.scales[h]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  const auto exponent_of = [&](const u4 (&x)[kQueriesFirst ? 1 : kSteps]) {
+    uint32_t top = 0;
+    if constexpr (BF16) {
+#pragma unroll
+      for (const u4& w : x) top = larger(top, w);
+      return exponent(top);
+    }
+    return 0;
   };
   if constexpr (kQueriesInLds) {
-    for (int n = wave; n < NQ; n += kW) {
-      h8 q[kSteps];
-      const float factor = load_queries(n, q);
+    if constexpr (!kQueriesFirst) {
+      if (wave < NQ) {
+        const int e2 = exponent_of(raw[0]);
 #pragma unroll
-      for (int c = 0; c < kSteps; ++c) sh.q[(n * kSteps + c) * 64 + lane] = __builtin_bit_cast(u4, q[c]);
-      if (g == 0) fs[n * 16 + i] = factor;
+        for (int c = 0; c < kSteps; ++c)
+          sh.q[(wave * kSteps + c) * 64 + lane] = __builtin_bit_cast(u4, fragment(wave, raw[0][c], e2));
+        if (g == 0) fs[wave * 16 + i] = factor(e2);
+      }
     }
     __syncthreads();
 #pragma unroll
     for (int n = 0; n < NQ; ++n) f[n] = fs[n * 16 + i];
   } else {
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) f[n] = load_queries(n, qreg[n]);
+    for (int n = 0; n < NQ; ++n) {
+      const int e2 = exponent_of(raw[n]);
+#pragma unroll
+      for (int c = 0; c < kSteps; ++c) qreg[n][c] = fragment(n, raw[n][c], e2);
+      f[n] = factor(e2);
+    }
   }
   const auto query = [&](int n, int c) -> h8 {
     if constexpr (kQueriesInLds)
@@ -403,88 +556,46 @@ __global__ __launch_bounds__(kW * 64, waves_per_simd(DIM, NQ)) void kv4_attentio
   };
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
-    pos[n] = s.len - s.ql + (row0 + n * 16 + i) / a.group;
     m[n] = kNoToken;
     l[n] = 0.f;
 #pragma unroll
     for (int j = 0; j < kBlocks; ++j) o[n][j] = f4{0.f, 0.f, 0.f, 0.f};
   }
 
-  // The unit's tiles, cut to what this row tile's rows see at all.
-  const int first_pos = s.len - s.ql + row0 / a.group, last_pos = s.len - s.ql + (row0 + nrows - 1) / a.group;
-  const int win = a.window;
-  int t0 = s.lo + split * chunk, t1 = min(t0 + chunk, s.lo + s.tiles);
-  t1 = min(t1, last_pos / kTileTokens + (last_pos >= 0));
-  if (win) t0 = max(t0, max(0, first_pos - win + 1) / kTileTokens);
-  const int mine = t1 > t0 + wave && a.pages > 0 ? (t1 - t0 - wave + kW - 1) / kW : 0;  // this wavefront's tiles
-  const int page = 1 << a.page_shift;
-  const int32_t* table = a.table + static_cast<int64_t>(b) * a.table_stride;
-  const uint8_t* head_base = a.cache + static_cast<int64_t>(head) * a.seg_bytes;
-
-  // Page indices of the wavefront's next 64 tiles, one lane each; -1: none.
-  int pid[2] = {-1, -1};
-  auto pages_from = [&](int j0) {
-    const int j = j0 + lane;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int tok = (t0 + wave + j * kW) * kTileTokens + 16 * h;
-      int p = -1;
-      if (j < mine && tok < s.len) p = table[tok >> a.page_shift];
-      pid[h] = p >= 0 && p < a.pages ? p : -1;
-    }
-  };
-  // Keys and values of tile j, the pages having been looked up.
-  Tile<DIM> t;
-  int pg[2] = {-1, -1};   // the pages of the tile in hand
-  const auto token_of = [&](int j) { return (t0 + wave + j * kW) * kTileTokens; };
-  const auto segment = [&](int p) {
-    return segment_of(head_base + static_cast<int64_t>(max(p, 0)) * a.page_bytes, a.seg_bytes);
-  };
-  auto look_up = [&](int (&next)[2], int j) {
-    if ((j & 63) == 0) pages_from(j);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) next[h] = __builtin_amdgcn_readlane(pid[h], j & 63);
-  };
-  auto keys = [&](const int (&p)[2], int j) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      load_keys<DIM>(t, h, segment(p[h]), (token_of(j) + 16 * h) & (page - 1), page, lane);
-  };
-  auto vals = [&](const int (&p)[2], int j) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      load_vals<DIM>(t, h, segment(p[h]), (token_of(j) + 16 * h) & (page - 1), page, lane);
-  };
-  if (mine > 0) {
-    look_up(pg, 0);
-    keys(pg, 0);
-    vals(pg, 0);
-  }
   // The keys of the next tile are on their way during this one's softmax and
   // values, its values during the next one's scores: one set of registers
   // each, and the other wavefronts of the SIMD to fill what is left.
+  //
+  // A SIMD serves the older of its wavefronts first, and the workgroup that
+  // came second to a compute unit would end a third later than the first. So
+  // a wavefront's priority falls with every quarter of its tiles: whoever is
+  // behind goes first.
+  const int quarter = (mine + 3) / 4;
+  __builtin_amdgcn_s_setprio(3);
   for (int j = 0; j < mine; ++j) {
-    const int tok = token_of(j);
+    if (j == quarter) __builtin_amdgcn_s_setprio(2);
+    if (j == 2 * quarter) __builtin_amdgcn_s_setprio(1);
+    if (j == 3 * quarter) __builtin_amdgcn_s_setprio(0);
+    const int tok = (t0 + wave + j * kW) * kTileTokens;
     f4 sc[2][NQ];
     scores<DIM, NQ>(t, query, sc);
+    const bool none0 = absent[0] >> (j & 63) & 1, none1 = absent[1] >> (j & 63) & 1;
     __builtin_amdgcn_sched_barrier(0);
-    int next[2] = {-1, -1};
-    if (j + 1 < mine) {
-      look_up(next, j + 1);
-      keys(next, j + 1);
-    }
+    const Place r = place(j + 1);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) load_keys<DIM>(t, h, r.seg[h], lane_at, r.codes[h], r.scales[h]);
     __builtin_amdgcn_sched_barrier(0);
     uint32_t vs[2] = {t.vs[0], t.vs[1]};
     const bool whole =
-        tok + kTileTokens - 1 <= first_pos && (win == 0 || tok > last_pos - win) && pg[0] >= 0 && pg[1] >= 0;
+        tok + kTileTokens - 1 <= first_pos && (win == 0 || tok > last_pos - win) && !none0 && !none1;
     if (!whole) {
       // Scores of unseen tokens become -inf whatever the cache holds there,
       // and the values of tokens past the end or of absent pages are zeroed:
       // such bytes may decode to NaN, which a p of 0 would not remove. Bit b
       // of a mask stands for token tok + 4 g + b.
-      const int at = tok + 4 * g;
+      const int mine0 = tok + 4 * g;
       const auto up_to = [](int x) -> uint32_t { return x < 0 ? 0u : x >= 31 ? ~0u : (2u << x) - 1u; };
-      const uint32_t held = up_to(s.len - 1 - at) & ((pg[0] >= 0 ? 0xFFFFu : 0u) | (pg[1] >= 0 ? 0xFFFF0000u : 0u));
+      const uint32_t held = up_to(s.len - 1 - mine0) & ((none0 ? 0u : 0xFFFFu) | (none1 ? 0u : 0xFFFF0000u));
       const auto bit = [](uint32_t w, int b) { return static_cast<uint32_t>(static_cast<int32_t>(w << (31 - b)) >> 31); };
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -492,7 +603,9 @@ __global__ __launch_bounds__(kW * 64, waves_per_simd(DIM, NQ)) void kv4_attentio
         for (int e = 0; e < 4; ++e) vs[h] &= ~(0xFFu << (8 * e)) | bit(held, 16 * h + e);
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
-        const uint32_t seen = held & up_to(pos[n] - at) & (win ? ~up_to(pos[n] - win - at) : ~0u);
+        // (the row's position is worked out here, for the few tiles that need it)
+        const int pos = s.len - s.ql + (row0 + n * 16 + i) / a.group;
+        const uint32_t seen = held & up_to(pos - mine0) & (win ? ~up_to(pos - win - mine0) : ~0u);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -536,11 +649,12 @@ __global__ __launch_bounds__(kW * 64, waves_per_simd(DIM, NQ)) void kv4_attentio
     }
     values<DIM, NQ>(t, vs, p, o);
     __builtin_amdgcn_sched_barrier(0);
-    if (j + 1 < mine) vals(next, j + 1);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) load_vals<DIM>(t, h, r.seg[h], lane_at, r.codes[h], r.scales[h]);
     __builtin_amdgcn_sched_barrier(0);
-    pg[0] = next[0], pg[1] = next[1];
   }
 
+  const AttnParams& z = reread(params);
   // Join the wavefronts: a row's reference becomes the largest of the four.
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
@@ -549,7 +663,7 @@ __global__ __launch_bounds__(kW * 64, waves_per_simd(DIM, NQ)) void kv4_attentio
     if (g == 0) ml[wave][n * 16 + i] = float2{m[n], l[n]};
   }
   __syncthreads();
-  const int64_t part_rows = static_cast<int64_t>(unit) * kRows;
+  const int64_t part_rows = static_cast<int64_t>(2 * group_id + (tile0 == 0)) * kRows;
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     float mx = ml[0][n * 16 + i].x;
@@ -564,7 +678,6 @@ __global__ __launch_bounds__(kW * 64, waves_per_simd(DIM, NQ)) void kv4_attentio
             f4{o[n][d][r] * down, o[n][d + 1][r] * down, o[n][d + 2][r] * down, o[n][d + 3][r] * down};
     __syncthreads();
     // 8 elements a thread
-#pragma unroll
     for (int x = tid; x < 16 * DIM / 8; x += kW * 64) {
       const int r = x / (DIM / 8), d = x % (DIM / 8) * 8, row = n * 16 + r;
       if (row < nrows) {
@@ -581,51 +694,61 @@ __global__ __launch_bounds__(kW * 64, waves_per_simd(DIM, NQ)) void kv4_attentio
 #pragma unroll
           for (int w = 1; w < kW; ++w) v[e] += red[w][r][d + e];
         }
-        if (splits > 1) {
-          float* dst = a.part + (part_rows + row) * DIM + d;
+        if (!alone) {
+          float* dst = z.part + (part_rows + row) * DIM + d;
           *reinterpret_cast<f4*>(dst) = f4{v[0], v[1], v[2], v[3]};
           *reinterpret_cast<f4*>(dst + 4) = f4{v[4], v[5], v[6], v[7]};
           if (d == 0) {
-            float2* mld = reinterpret_cast<float2*>(a.part + a.max_units * kRows * DIM);
+            float2* mld = reinterpret_cast<float2*>(z.part + static_cast<int64_t>(2 * z.groups) * kRows * DIM);
             mld[part_rows + row] = float2{mr, lr};
           }
         } else {
-          const int qi = (row0 + row) / a.group, hh = (row0 + row) - qi * a.group;
-          const int64_t at = static_cast<int64_t>(s.qs + qi) * (a.kv_heads * a.group) + head * a.group + hh;
-          const float up = lr > 0.f ? a.v_scale / lr : (lr == 0.f ? 0.f : lr);
+          const int qi = (row0 + row) / z.group, hh = (row0 + row) - qi * z.group;
+          const int64_t row_at = static_cast<int64_t>(s.qs + qi) * (z.kv_heads * z.group) + head * z.group + hh;
+          const float up = lr > 0.f ? z.v_scale / lr : (lr == 0.f ? 0.f : lr);
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[e] *= up;
-          store_out8<BF16>(a.out, at * DIM + d, v);
-          if (d == 0 && a.lse)
-            a.lse[at] = lr == 0.f ? -__builtin_inff() : (__builtin_amdgcn_logf(lr) + mr) * 0.69314718055994531f;
+          store_out8<BF16>(z.out, row_at * DIM + d, v);
+          if (d == 0 && z.lse)
+            z.lse[row_at] = lr == 0.f ? -__builtin_inff() : (__builtin_amdgcn_logf(lr) + mr) * 0.69314718055994531f;
         }
       }
     }
     __syncthreads();
   }
+  }
+  if (at >= end) break;
+  if (at - base >= cost * s.rt * reread(params).kv_heads) {
+    // the next sequence that has rows
+    base = at;
+    do ++b;
+    while (sequence(reread(params), b, kRows).rt == 0);
+  }
+  }
 }
 
-// Joins the units of the sequences that were cut: one wavefront a (row, query
-// head), in the order of the units.
+// Joins the pieces of the runs that were cut: one wavefront a (row, query
+// head), the pieces in the order of the line.
 template <int DIM, bool BF16>
 __global__ __launch_bounds__(256) void kv4_attention_join_kernel(const AttnParams a, int unit_rows) {
-  constexpr int kPer = 8, kLanes = DIM / kPer;  // lanes that hold a row; the others take other units
+  constexpr int kPer = 8, kLanes = DIM / kPer;  // lanes that hold a row; the others take other pieces
   constexpr int kGroups = 64 / kLanes;
   const int lane = threadIdx.x & 63;
   const int64_t id = static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int heads = a.kv_heads * a.group;
   if (id >= static_cast<int64_t>(a.rows) * heads) return;
   const int row = static_cast<int>(id / heads), head = static_cast<int>(id - static_cast<int64_t>(row) * heads);
-  int b, qs;
+  const int share = a.sched[a.batch].x;
+  int b = 0, qs;
   if (a.q_start) {
     // the last sequence that starts at or before the row
-    int lo = 0, hi = a.batch - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      if (a.q_start[mid] <= row) lo = mid;
-      else hi = mid - 1;
+    for (int b0 = 0; b0 < a.batch; b0 += 64) {
+      const bool before = b0 + lane < a.batch && a.q_start[b0 + lane] <= row;
+      const unsigned long long m = __ballot(before);
+      if (m) b = b0 + 63 - __builtin_clzll(m);
+      if (m != ~0ull) break;
     }
-    b = lo;
+    b = __builtin_amdgcn_readfirstlane(b);
     qs = a.q_start[b];
     if (row < qs || row - qs >= a.max_q || row >= a.q_start[b + 1]) return;  // a row of no sequence
   } else {
@@ -633,30 +756,29 @@ __global__ __launch_bounds__(256) void kv4_attention_join_kernel(const AttnParam
     qs = b * a.max_q;
   }
   const int4 sc = a.sched[b];
-  if (sc.y <= 1) return;  // written by its only unit
   const int r = (row - qs) * a.group + head % a.group;
-  const int rtile = r / unit_rows;
-  const int step = sc.z * a.kv_heads;
-  const int64_t first = sc.x + rtile * a.kv_heads + head / a.group;
-  const float2* ml = reinterpret_cast<const float2*>(a.part + a.max_units * unit_rows * DIM) + r % unit_rows;
+  const int first = sc.x + (r / unit_rows * a.kv_heads + head / a.group) * (sc.y + kRunCost) + kRunCost;
+  const int w0 = first / share, w1 = (first + sc.y - 1) / share;
+  if (w0 == w1) return;  // written by the workgroup that had all of it
+  const float2* ml = reinterpret_cast<const float2*>(a.part + static_cast<int64_t>(2 * a.groups) * unit_rows * DIM);
+  const auto piece = [&](int w) { return static_cast<int64_t>(2 * w + (w == w0)) * unit_rows + r % unit_rows; };
   float mx = kNoToken;
-  for (int s = lane; s < sc.y; s += 64) mx = fmaxf(mx, ml[(first + static_cast<int64_t>(s) * step) * unit_rows].x);
+  for (int w = w0 + lane; w <= w1; w += 64) mx = fmaxf(mx, ml[piece(w)].x);
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
   float l = 0.f, v[kPer] = {};
   const int gr = lane / kLanes, d = lane % kLanes * kPer;
 #pragma unroll 4
-  for (int s = gr; s < sc.y; s += kGroups) {
-    const int64_t at = (first + static_cast<int64_t>(s) * step) * unit_rows;
-    const float2 x = ml[at];
-    const float* src = a.part + (at + r % unit_rows) * DIM + d;
+  for (int w = w0 + gr; w <= w1; w += kGroups) {
+    const float2 x = ml[piece(w)];
+    const float* src = a.part + piece(w) * DIM + d;
     const f4 v0 = *reinterpret_cast<const f4*>(src), v1 = *reinterpret_cast<const f4*>(src + 4);
-    const float w = __builtin_amdgcn_exp2f(x.x - mx);
-    l += w * x.y;
+    const float p = __builtin_amdgcn_exp2f(x.x - mx);
+    l += p * x.y;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      v[e] += w * v0[e];
-      v[4 + e] += w * v1[e];
+      v[e] += p * v0[e];
+      v[4 + e] += p * v1[e];
     }
   }
 #pragma unroll
@@ -676,11 +798,10 @@ __global__ __launch_bounds__(256) void kv4_attention_join_kernel(const AttnParam
 
 template <int DIM, int NQ, bool BF16>
 hipError_t launch_as(const AttnParams& a, hipStream_t stream) {
-  kv4_attention_kernel<DIM, NQ, BF16><<<dim3(static_cast<uint32_t>(a.max_units)), dim3(kW * 64), 0, stream>>>(a);
+  const uint32_t grid = a.groups ? a.groups : static_cast<uint32_t>(a.batch) * a.row_tiles * a.kv_heads;
+  kv4_attention_kernel<DIM, NQ, BF16><<<dim3(grid), dim3(kW * 64), 0, stream>>>(a);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  // a sequence of at most min_chunk tiles is one unit
-  if (a.max_kv <= a.min_chunk * kTileTokens) return hipSuccess;
+  if (e != hipSuccess || a.groups == 0) return e;
   const int64_t heads = static_cast<int64_t>(a.rows) * a.kv_heads * a.group;
   kv4_attention_join_kernel<DIM, BF16>
       <<<dim3(static_cast<uint32_t>((heads + 3) / 4)), dim3(256), 0, stream>>>(a, 16 * NQ);
@@ -730,7 +851,7 @@ hipError_t launch_kv4_attention(const qpn_kv4_cache& c, const qpn_kv4_attention_
   a.kv_len = x.kv_len, a.q_start = x.q_start;
   a.batch = x.batch, a.rows = x.rows, a.max_q = x.max_q_len < x.rows ? x.max_q_len : x.rows;
   a.max_kv = x.max_kv_len, a.window = x.window;
-  a.slots = p.slots, a.min_chunk = p.min_chunk, a.max_units = p.max_units;
+  a.row_tiles = p.row_tiles, a.groups = p.groups, a.min_share = p.min_share;
   a.f = x.scale * 1.44269504088896341f * c.k_scale;
   a.v_scale = c.v_scale;
   a.sched = static_cast<int4*>(workspace);

@@ -11,6 +11,7 @@ current stream only; every step runs in the library's HIP kernels.
 that share pages, copies on write, release and compaction.
 """
 
+import functools
 import math
 
 import torch
@@ -31,9 +32,14 @@ from .decode import (
     qpn_verify_args,
     qpn_verify_workspace_bytes,
 )
-from .torch_api import _output, _stream
 
 DTYPES = {torch.float16: QPN_DT_F16, torch.bfloat16: QPN_DT_BF16, torch.float32: QPN_DT_F32}
+HALVES = (torch.float16, torch.bfloat16)
+
+# A verify step makes these calls once a layer, so what Python adds to each
+# counts: checks compare plain attributes, the descriptors of a cache are built
+# once, and the current stream is taken as the raw handle that torch keeps.
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _on_device(t, name, device=None):
@@ -41,45 +47,52 @@ def _on_device(t, name, device=None):
         raise ValueError(f"{name} must be a CUDA tensor")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
-    return t
 
 
-def _ints(t, dtype, shape, name, device):
-    """A contiguous tensor of whole numbers of exactly this shape."""
-    _on_device(t, name, device)
-    if t.dtype != dtype or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+def _exactly(t, dtype, shape, name, device):
+    """A contiguous tensor of this type and shape; returns its address."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and t.device == device):
+        _on_device(t, name, device)
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, not {t.dtype} "
                          f"{tuple(t.shape)}")
-    return t
-
-
-def _floats(t, shape, name, device):
-    _on_device(t, name, device)
-    if t.dtype != torch.float32 or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {tuple(shape)}, not {t.dtype} "
-                         f"{tuple(t.shape)}")
-    return t
+    return t.data_ptr()
 
 
 def _rows(t, shape, name, device, dtypes):
-    """A tensor of this shape whose last dimension is contiguous, other strides free."""
-    _on_device(t, name, device)
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name} must be one of {', '.join(str(d) for d in dtypes)}, not {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    """A tensor of this shape whose last dimension is contiguous, other strides
+    free; returns its address and those strides."""
+    if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.device == device):
+        _on_device(t, name, device)
+        if t.dtype not in dtypes:
+            raise ValueError(f"{name} must be one of {', '.join(str(d) for d in dtypes)}, not {t.dtype}")
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
+    st = t.stride()
+    if st[2] != 1 and t.shape[2] > 1 and t.numel():
         raise ValueError(f"{name}'s last dimension must be contiguous")
+    return t.data_ptr(), st[0], st[1]
+
+
+def _out(t, dtype, shape, name, device):
+    """The caller's output, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _exactly(t, dtype, shape, name, device)
     return t
 
 
 def _workspace(need, workspace, device):
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    """(tensor, address, bytes) of the caller's workspace where it is large
+    enough, or of a new one."""
     if not need:
-        return None, 0
-    _on_device(workspace, "workspace", device)
-    return workspace, workspace.numel() * workspace.element_size()
+        return None, None, 0
+    if workspace is not None:
+        _on_device(workspace, "workspace", device)
+        have = workspace.numel() * workspace.element_size()
+        if have >= need:
+            return workspace, workspace.data_ptr(), have
+    workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace, workspace.data_ptr(), need
 
 
 class KV4Cache:
@@ -120,19 +133,21 @@ class KV4Cache:
             raise ValueError("k_scale and v_scale take one number, or one a layer")
         if not all(math.isfinite(s) and s > 0 for s in self.k_scale + self.v_scale):
             raise ValueError("tensor scales must be finite and above 0")
-
-    @property
-    def device(self):
-        return self.data.device
-
-    def layer(self, layer):
-        if not 0 <= layer < self.layers:
-            raise ValueError(f"layer must be 0 .. {self.layers - 1}, not {layer}")
-        return layer
+        self.k_scale, self.v_scale = tuple(self.k_scale), tuple(self.v_scale)  # the descriptors hold them
+        self.device = data.device
+        self._descs = [None] * self.layers
 
     def desc(self, layer=0):
-        return qpn_kv4_cache(self.data.data_ptr(), self.pages, self.layers, self.page_size, self.kv_heads,
-                             self.head_dim, self.k_scale[layer], self.v_scale[layer])
+        """The C descriptor with one layer's scales."""
+        if not 0 <= layer < self.layers:
+            raise ValueError(f"layer must be 0 .. {self.layers - 1}, not {layer}")
+        d = self._descs[layer]
+        if d is None:
+            _on_device(self.data, "the cache's data")
+            d = self._descs[layer] = qpn_kv4_cache(self.data.data_ptr(), self.pages, self.layers, self.page_size,
+                                                   self.kv_heads, self.head_dim, self.k_scale[layer],
+                                                   self.v_scale[layer])
+        return d
 
 
 def kv4_append(cache, k, v, slots, layer=0):
@@ -140,12 +155,14 @@ def kv4_append(cache, k, v, slots, layer=0):
     strides with a contiguous last dimension: slices of a fused projection's
     output will do) into the pages' slots (int64 [tokens], page * page_size +
     offset; one outside the pool is skipped)."""
-    shape = (slots.shape[0], cache.kv_heads, cache.head_dim)
-    _rows(k, shape, "k", cache.device, (torch.float16, torch.bfloat16))
-    _rows(v, shape, "v", cache.device, (k.dtype,))
-    _ints(slots, torch.int64, (shape[0],), "slots", cache.device)
-    qpn_kv4_append(cache.desc(cache.layer(layer)), layer, k.data_ptr(), v.data_ptr(), DTYPES[k.dtype], shape[0],
-                   k.stride(0), k.stride(1), v.stride(0), v.stride(1), slots.data_ptr(), _stream())
+    dev = cache.device
+    tokens = slots.shape[0]
+    shape = (tokens, cache.kv_heads, cache.head_dim)
+    kp, kt, kh = _rows(k, shape, "k", dev, HALVES)
+    vp, vt, vh = _rows(v, shape, "v", dev, (k.dtype,))
+    sp = _exactly(slots, torch.int64, (tokens,), "slots", dev)
+    qpn_kv4_append(cache.desc(layer), layer, kp, vp, DTYPES[k.dtype], tokens, kt, kh, vt, vh, sp,
+                   _raw_stream(dev.index))
 
 
 def kv4_read(cache, slots, layer=0, dtype=torch.float16, k=None, v=None):
@@ -153,13 +170,14 @@ def kv4_read(cache, slots, layer=0, dtype=torch.float16, k=None, v=None):
     [tokens]) stand for, zeros for one outside the pool."""
     if dtype not in DTYPES:
         raise ValueError(f"dtype must be one of {', '.join(str(d) for d in DTYPES)}, not {dtype}")
-    _on_device(slots, "slots", cache.device)
-    _ints(slots, torch.int64, (slots.numel(),), "slots", cache.device)
-    shape = (slots.shape[0], cache.kv_heads, cache.head_dim)
-    k = _output(k, shape, dtype, cache.data, "k")
-    v = _output(v, shape, dtype, cache.data, "v")
-    qpn_kv4_read(cache.desc(cache.layer(layer)), layer, slots.data_ptr(), shape[0], DTYPES[dtype], k.data_ptr(),
-                 v.data_ptr(), _stream())
+    dev = cache.device
+    tokens = slots.shape[0]
+    sp = _exactly(slots, torch.int64, (tokens,), "slots", dev)
+    shape = (tokens, cache.kv_heads, cache.head_dim)
+    k = _out(k, dtype, shape, "k", dev)
+    v = _out(v, dtype, shape, "v", dev)
+    qpn_kv4_read(cache.desc(layer), layer, sp, tokens, DTYPES[dtype], k.data_ptr(), v.data_ptr(),
+                 _raw_stream(dev.index))
     return k, v
 
 
@@ -167,24 +185,27 @@ def kv4_copy_pages(cache, src, dst):
     """Copies pages src[i] onto dst[i] (int32 [n]) in every layer, in one
     launch. No page may be both a source and a destination, or a destination
     twice; a pair with a page outside the pool is skipped."""
-    _on_device(src, "src", cache.device)
-    _ints(src, torch.int32, (src.numel(),), "src", cache.device)
-    _ints(dst, torch.int32, tuple(src.shape), "dst", cache.device)
-    qpn_kv4_copy_pages(cache.desc(), src.data_ptr(), dst.data_ptr(), src.shape[0], _stream())
+    dev = cache.device
+    n = src.shape[0]
+    sp = _exactly(src, torch.int32, (n,), "src", dev)
+    dp = _exactly(dst, torch.int32, (n,), "dst", dev)
+    qpn_kv4_copy_pages(cache.desc(), sp, dp, n, _raw_stream(dev.index))
 
 
-def _attention_sizes(rows, heads, batch, max_q_len, max_kv_len):
+@functools.lru_cache(maxsize=256)
+def _attention_workspace_bytes(page_size, kv_heads, head_dim, rows, heads, batch, max_q_len, max_kv_len):
+    c = qpn_kv4_cache(None, 0, 1, page_size, kv_heads, head_dim, 1.0, 1.0)
     a = qpn_kv4_attention_args()
     a.heads, a.batch, a.rows, a.max_q_len, a.max_kv_len = heads, batch, rows, max_q_len, max_kv_len
-    return a
+    return qpn_kv4_attention_workspace_bytes(c, a)
 
 
 def kv4_attention_workspace(cache, rows, heads, batch, max_q_len, max_kv_len):
     """A workspace for kv4_attention with these sizes (None when none is
     needed). It carries nothing from call to call, but two calls that may run
     at once need one each."""
-    need = qpn_kv4_attention_workspace_bytes(cache.desc(),
-                                             _attention_sizes(rows, heads, batch, max_q_len, max_kv_len))
+    need = _attention_workspace_bytes(cache.page_size, cache.kv_heads, cache.head_dim, rows, heads, batch, max_q_len,
+                                      max_kv_len)
     return torch.empty(need, dtype=torch.uint8, device=cache.device) if need else None
 
 
@@ -197,52 +218,55 @@ def kv4_attention(q, cache, table, kv_len, q_start=None, max_q_len=None, max_kv_
     int32 [batch, pages a sequence at most]; kv_len int32 [batch]; q_start
     int32 [batch + 1] from 0 to rows, with max_q_len the longest (None: rows /
     batch rows each). max_kv_len bounds the lengths (default: what the table
-    can hold); a close bound spares a small call its second launch. window > 0:
-    a row sees the last `window` tokens up to its own. out [rows, heads,
-    head_dim] like q, lse fp32 [rows, heads]; a row that sees no token gets
-    zeros and -inf."""
-    _on_device(q, "q", cache.device)
+    can hold); a bound of 512 or less spares a small call its second launch.
+    window > 0: a row sees the last `window` tokens up to its own. out [rows,
+    heads, head_dim] like q, lse fp32 [rows, heads]; a row that sees no token
+    gets zeros and -inf."""
+    dev = cache.device
+    dim, kv_heads = cache.head_dim, cache.kv_heads
+    _on_device(q, "q", dev)
     if q.dim() != 3:
-        raise ValueError(f"q must have shape (rows, heads, {cache.head_dim}), not {tuple(q.shape)}")
-    rows, heads = q.shape[0], q.shape[1]
-    _rows(q, (rows, heads, cache.head_dim), "q", cache.device, (torch.float16, torch.bfloat16))
-    if heads == 0 or heads % cache.kv_heads:
-        raise ValueError(f"q's {heads} heads must be a multiple of the cache's {cache.kv_heads}")
-    _on_device(table, "table", cache.device)
-    if table.dim() != 2 or table.dtype != torch.int32 or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError(f"q must have shape (rows, heads, {dim}), not {tuple(q.shape)}")
+    rows, heads, _ = q.shape
+    qp, qt, qh = _rows(q, (rows, heads, dim), "q", dev, HALVES)
+    if heads == 0 or heads % kv_heads:
+        raise ValueError(f"q's {heads} heads must be a multiple of the cache's {kv_heads}")
+    _on_device(table, "table", dev)
+    if table.dtype is not torch.int32 or table.dim() != 2 or (table.stride(1) != 1 and table.shape[1] > 1):
         raise ValueError("table must be an int32 [batch, pages] tensor with contiguous rows")
-    batch = table.shape[0]
-    _ints(kv_len, torch.int32, (batch,), "kv_len", cache.device)
+    batch, held = table.shape
+    lp = _exactly(kv_len, torch.int32, (batch,), "kv_len", dev)
     if q_start is not None:
-        _ints(q_start, torch.int32, (batch + 1,), "q_start", cache.device)
+        sp = _exactly(q_start, torch.int32, (batch + 1,), "q_start", dev)
         if max_q_len is None:
             raise ValueError("q_start needs max_q_len, the longest sequence's rows")
     else:
+        sp = None
         each = rows // batch if batch else 0
         if each * batch != rows or (max_q_len is not None and max_q_len != each):
             raise ValueError(f"{rows} rows are not {batch} sequences of as many: give q_start and max_q_len")
         max_q_len = each
     if max_kv_len is None:
-        max_kv_len = table.shape[1] * cache.page_size
-    out = _output(out, (rows, heads, cache.head_dim), q.dtype, q)
-    lse = _output(lse, (rows, heads), torch.float32, q, "lse")
-    a = _attention_sizes(rows, heads, batch, max_q_len, max_kv_len)
-    a.q, a.out, a.lse = q.data_ptr(), out.data_ptr(), lse.data_ptr()
-    a.table, a.kv_len = table.data_ptr(), kv_len.data_ptr()
-    a.q_start = q_start.data_ptr() if q_start is not None else None
-    a.q_token_stride, a.q_head_stride = q.stride(0), q.stride(1)
-    a.table_stride = table.stride(0) if batch > 1 else table.shape[1]
-    a.dtype, a.layer, a.window = DTYPES[q.dtype], cache.layer(layer), window
-    a.scale = 1.0 / math.sqrt(cache.head_dim) if scale is None else scale
-    d = cache.desc(layer)
-    workspace, nbytes = _workspace(qpn_kv4_attention_workspace_bytes(d, a), workspace, q.device)
-    qpn_kv4_attention(d, a, workspace.data_ptr() if nbytes else None, nbytes, _stream())
+        max_kv_len = held * cache.page_size
+    out = _out(out, q.dtype, (rows, heads, dim), "out", dev)
+    lse = _out(lse, torch.float32, (rows, heads), "lse", dev)
+    a = qpn_kv4_attention_args(qp, out.data_ptr(), lse.data_ptr(), table.data_ptr(), lp, sp, qt, qh,
+                               table.stride(0) if batch > 1 else held, DTYPES[q.dtype], layer, heads, batch, rows,
+                               max_q_len, max_kv_len, window, dim ** -0.5 if scale is None else scale, 0)
+    workspace, wp, nbytes = _workspace(
+        _attention_workspace_bytes(cache.page_size, kv_heads, dim, rows, heads, batch, max_q_len, max_kv_len), workspace,
+        dev)
+    qpn_kv4_attention(cache.desc(layer), a, wp, nbytes, _raw_stream(dev.index))
     return out, lse
 
 
+_verify_workspace_bytes = functools.lru_cache(maxsize=256)(qpn_verify_workspace_bytes)
+
+
 def verify_workspace(batch, drafts, vocab, device="cuda"):
-    """A workspace for verify_drafts with these sizes."""
-    need = qpn_verify_workspace_bytes(batch, drafts, vocab)
+    """A workspace for verify_drafts with these sizes. It carries nothing from
+    call to call, but two calls that may run at once need one each."""
+    need = _verify_workspace_bytes(batch, drafts, vocab)
     return torch.empty(need, dtype=torch.uint8, device=device) if need else None
 
 
@@ -264,37 +288,27 @@ def verify_drafts(target, draft_tokens, u_accept, u_sample, draft=None, num_draf
     dev = target.device
     if target.dim() != 3:
         raise ValueError(f"target must have shape (batch, drafts + 1, vocab), not {tuple(target.shape)}")
-    batch, drafts, vocab = target.shape[0], target.shape[1] - 1, target.shape[2]
+    batch, places, vocab = target.shape
+    drafts = places - 1
     if drafts < 0:
         raise ValueError("target needs a row for the token after the drafts")
-    kinds = (torch.float32,) if probabilities else tuple(DTYPES)
-    _rows(target, (batch, drafts + 1, vocab), "target", dev, kinds)
-    if draft is not None:
-        _rows(draft, (batch, drafts, vocab), "draft", dev, (target.dtype,))
-    _ints(draft_tokens, torch.int32, (batch, drafts), "draft_tokens", dev)
-    _floats(u_accept, (batch, drafts), "u_accept", dev)
-    _floats(u_sample, (batch,), "u_sample", dev)
-    if num_draft is not None:
-        _ints(num_draft, torch.int32, (batch,), "num_draft", dev)
-    if temperature is not None:
+    tp, tb, tr = _rows(target, (batch, places, vocab), "target", dev, (torch.float32,) if probabilities else DTYPES)
+    dp, db, dr = (None, 0, 0) if draft is None else _rows(draft, (batch, drafts, vocab), "draft", dev, (target.dtype,))
+    np_ = None if num_draft is None else _exactly(num_draft, torch.int32, (batch,), "num_draft", dev)
+    if temperature is None:
+        tmp = None
+    else:
         if probabilities:
             raise ValueError("probabilities are taken as they are: no temperature")
-        _floats(temperature, (batch,), "temperature", dev)
-    tokens = _output(tokens, (batch, drafts + 1), torch.int32, target, "tokens")
-    accepted = _output(accepted, (batch,), torch.int32, target, "accepted")
-    logprobs = _output(logprobs, (batch, drafts + 1), torch.float32, target, "logprobs")
-    a = qpn_verify_args()
-    a.target, a.draft = target.data_ptr(), draft.data_ptr() if draft is not None else None
-    a.draft_tokens = draft_tokens.data_ptr()
-    a.num_draft = num_draft.data_ptr() if num_draft is not None else None
-    a.temperature = temperature.data_ptr() if temperature is not None else None
-    a.u_accept, a.u_sample = u_accept.data_ptr(), u_sample.data_ptr()
-    a.tokens, a.accepted, a.logprobs = tokens.data_ptr(), accepted.data_ptr(), logprobs.data_ptr()
-    a.target_batch_stride, a.target_row_stride = target.stride(0), target.stride(1)
-    if draft is not None:
-        a.draft_batch_stride, a.draft_row_stride = draft.stride(0), draft.stride(1)
-    a.dtype, a.probabilities = DTYPES[target.dtype], int(probabilities)
-    a.batch, a.drafts, a.vocab = batch, drafts, vocab
-    workspace, nbytes = _workspace(qpn_verify_workspace_bytes(batch, drafts, vocab), workspace, dev)
-    qpn_verify(a, workspace.data_ptr() if nbytes else None, nbytes, _stream())
+        tmp = _exactly(temperature, torch.float32, (batch,), "temperature", dev)
+    tokens = _out(tokens, torch.int32, (batch, places), "tokens", dev)
+    accepted = _out(accepted, torch.int32, (batch,), "accepted", dev)
+    logprobs = _out(logprobs, torch.float32, (batch, places), "logprobs", dev)
+    a = qpn_verify_args(tp, dp, _exactly(draft_tokens, torch.int32, (batch, drafts), "draft_tokens", dev), np_, tmp,
+                        _exactly(u_accept, torch.float32, (batch, drafts), "u_accept", dev),
+                        _exactly(u_sample, torch.float32, (batch,), "u_sample", dev), tokens.data_ptr(),
+                        accepted.data_ptr(), logprobs.data_ptr(), tb, tr, db, dr, DTYPES[target.dtype],
+                        1 if probabilities else 0, batch, drafts, vocab, 0)
+    workspace, wp, nbytes = _workspace(_verify_workspace_bytes(batch, drafts, vocab), workspace, dev)
+    qpn_verify(a, wp, nbytes, _raw_stream(dev.index))
     return tokens, accepted, logprobs

@@ -205,7 +205,11 @@ def test_torch_layer_refuses_cpu_tensors_and_bad_caches():
     with pytest.raises(ValueError):
         qd.KV4Cache.wrap(torch.zeros((1, 2, 100), dtype=torch.uint8), 16, 2, 64)
     cache = qd.KV4Cache(4, 16, 2, 64, layers=2, k_scale=[0.5, 0.25], device="cpu")
-    assert cache.desc(1).k_scale == 0.25 and cache.desc(1).layers == 2
+    assert cache.k_scale == (0.5, 0.25) and cache.layers == 2
+    with pytest.raises(ValueError, match="layer"):
+        cache.desc(2)
+    with pytest.raises(ValueError, match="CUDA"):
+        cache.desc(1)
     x = torch.zeros((3, 2, 64), dtype=torch.float16)
     slots = torch.zeros(3, dtype=torch.int64)
     with pytest.raises(ValueError, match="CUDA"):

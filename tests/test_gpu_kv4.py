@@ -372,7 +372,7 @@ def test_attention_layers_uniform_blocks_and_bounds():
     caller's outputs and workspace, and a table that is a slice."""
     c = Case(19, [120, 33, 64], [4, 4, 4], 8, 4, 128, 32, "fp16", layers=3, layer=2)
     cache, table, kv_len, _ = c.device()
-    cache.k_scale, cache.v_scale = [9.0, 9.0, c.k_scale], [9.0, 9.0, c.v_scale]
+    cache = qd.KV4Cache.wrap(cache.data, 32, 4, 128, [9.0, 9.0, c.k_scale], [9.0, 9.0, c.v_scale])
     wide = torch.full((3, table.shape[1] + 5), 7, dtype=torch.int32, device=DEV)
     wide[:, :table.shape[1]] = table
     q = c.q.to(DEV)

@@ -156,7 +156,9 @@ typedef struct {
   int32_t reserved;             /* 0 */
 } qpn_verify_args;
 
-/* Workspace of a call with these sizes (0 for sizes that are refused). */
+/* Workspace of a call with these sizes (0 for sizes that are refused: more
+ * rows and chunks of 4096 tokens than a launch has workgroups for). Its
+ * contents need no preparation and carry nothing to the next call. */
 size_t qpn_verify_workspace_bytes(int32_t batch, int32_t drafts, int32_t vocab);
 
 qpn_status qpn_verify(const qpn_verify_args* args, void* workspace_dev, size_t workspace_bytes, void* stream);

@@ -144,13 +144,16 @@ qpn_status check_kv4_attention(const qpn_kv4_cache* c, const qpn_kv4_attention_a
 bool plan_verify(int32_t batch, int32_t drafts, int32_t vocab, VerifyPlan* p) {
   if (batch < 0 || batch > 65536 || drafts < 0 || drafts > 64 || vocab < 1 || vocab > (1 << 24)) return false;
   p->chunk = 4096;
-  // a row may begin up to 7 elements into its first 16-byte vector
-  p->chunks = (vocab + 7 + p->chunk - 1) / p->chunk;
+  p->chunks = (vocab + p->chunk - 1) / p->chunk;
   const size_t rows = static_cast<size_t>(batch) * (2 * drafts + 1);
-  if (rows * p->chunks > static_cast<size_t>(kMaxGroups)) return false;
+  // (a launch of 1024-thread workgroups a chunk, too)
+  if (rows * p->chunks > static_cast<size_t>(kMaxGroups) ||
+      static_cast<size_t>(batch) * p->chunks > static_cast<size_t>(kMaxGroups) / 4)
+    return false;
+  p->verdict_bytes = static_cast<size_t>(batch) * 32;
   p->stat_bytes = rows * p->chunks * 16;
-  p->sum_bytes = static_cast<size_t>(batch) * p->chunks * 3 * sizeof(double);
-  p->total_bytes = p->stat_bytes + round16(p->sum_bytes);
+  p->total_bytes = p->verdict_bytes + p->stat_bytes +
+                   round16(static_cast<size_t>(batch) * p->chunks * 3 * sizeof(double));
   return true;
 }
 

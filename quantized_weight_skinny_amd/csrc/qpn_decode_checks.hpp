@@ -44,7 +44,7 @@ qpn_status check_kv4_attention(const qpn_kv4_cache* c, const qpn_kv4_attention_a
 // `chunk` elements.
 struct VerifyPlan {
   int chunk, chunks;
-  size_t stat_bytes, sum_bytes, total_bytes;
+  size_t verdict_bytes, stat_bytes, total_bytes;
 };
 
 bool plan_verify(int32_t batch, int32_t drafts, int32_t vocab, VerifyPlan* p);

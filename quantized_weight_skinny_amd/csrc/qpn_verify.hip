@@ -5,22 +5,33 @@
 // that is all the accept tests need. Only one row a sequence (two with a
 // draft) is then read again, for the place of u_sample among the running
 // sums. A vocabulary's running sums lie closer together than 32 bits tell
-// apart, so these weights and sums are 64-bit, spread over the workgroups in
-// chunks: chunk sums, then (with a draft's logits) the chunk sums of
-// max(p - q, 0), for which both rows' totals must be known, then one
-// workgroup a sequence finds the chunk and the token in it. The kernels after
-// the first repeat the accept tests, a few hundred values from the cache,
-// instead of handing them over in a launch of their own.
+// apart, so these weights and sums are 64-bit, a chunk a workgroup: the chunk
+// sums of p and q; then, for a rejected draft with a row of its own, those of
+// max(p - q, 0), for which both totals must be known; then one workgroup a
+// sequence finds the chunk and the token in it.
+//
+// These kernels are short, and most of their time is latency. For few
+// sequences the accept tests are repeated by every workgroup of the second
+// pass, 16 wavefronts for its rows at once, instead of taking a launch. (The last workgroup of
+// each row and sequence, found by a counter, making them in the first pass
+// measured 13.6 us instead of 5.0 for 8 rows, and 52 instead of 32 for 480:
+// the counter's round trip is added to every workgroup.) And a launch fetches
+// each line of its code from memory, so a kernel of few workgroups holds one
+// copy of the 64-bit exponential, in a loop (the last pass 16.8 -> 12.6 us).
 #include "qpn_decode_internal.hpp"
 #include "qpn_device.hpp"
 
 namespace qpn {
 namespace {
 
-constexpr int kT = 256;          // threads
+constexpr int kT = 256;          // threads of the first pass
 constexpr int kChunk = 4096;     // elements a workgroup takes of a row
 constexpr int kPer = kChunk / kT;
+constexpr int kD = 1024;         // threads of the passes that draw
+constexpr int kDrawPer = kChunk / kD;
+constexpr int kDrawWaves = kD / 64;
 constexpr int kMaxDrafts = 64;
+typedef u4 u4_anywhere __attribute__((aligned(2)));
 
 struct Stat {
   float max;
@@ -29,11 +40,23 @@ struct Stat {
 };
 static_assert(sizeof(Stat) == 16, "the workspace holds 16 bytes a chunk");
 
+// What the accept tests leave to the passes that draw a token.
+enum : int { kDone = 0, kFromP = 1, kFromRest = 2 };
+struct Verdict {
+  int accepted, how;
+  int skip;             // the rejected draft, struck from p where no draft row is given; -1: none
+  float t;              // the temperature (1 for probabilities)
+  float p_max, q_max;   // maxima of the rows that the token is picked from
+  int pad[2];
+};
+static_assert(sizeof(Verdict) == 32, "the workspace holds 32 bytes a sequence");
+
 struct VerifyParams {
   qpn_verify_args a;
-  int chunks;
-  Stat* stats;   // [batch][drafts + 1][chunks], then [batch][drafts][chunks]
-  double* sums;  // [batch][3][chunks]: of p, of q, of what q leaves over
+  int chunks, decided;
+  Verdict* verdicts;  // [batch]
+  Stat* stats;        // [batch][drafts + 1][chunks], then [batch][drafts][chunks]
+  double* sums;       // [batch][3][chunks]: of p, of q, of what q leaves over
 };
 
 template <typename T>
@@ -114,39 +137,151 @@ __device__ __forceinline__ float temperature_of(const VerifyParams& p, int b) {
   return t > 0.f ? t : 0.f;
 }
 
-// Maximum and sum of exponentials of one chunk of one row. The chunk grid is
-// laid on 16-byte boundaries of memory, so that rows of any alignment are
-// read in whole vectors but for their first and last.
+// log x for x > 0, to 32 bits.
+__device__ __forceinline__ float log_of(double x) {
+  const float m = __builtin_amdgcn_logf(static_cast<float>(__builtin_amdgcn_frexp_mant(x)));
+  return (static_cast<float>(__builtin_amdgcn_frexp_exp(x)) + m) * 0.69314718055994531f;
+}
+
+// One row's chunks as one, by a wavefront (all its lanes return it).
+__device__ __forceinline__ Stat join_stats(const Stat* s, int chunks, float scale) {
+  const int lane = threadIdx.x & 63;
+  Stat r{-__builtin_inff(), 0x7FFFFFFF, 0.0};
+  // e^((x - m) / t) for two maxima; 0 for -inf, also under -inf
+  const auto ratio = [&](float x, float m) {
+    return x == -__builtin_inff() ? 0.f : x == m ? 1.f : __builtin_amdgcn_exp2f((x - m) * scale);
+  };
+#pragma unroll 1
+  for (int c = lane; c < chunks; c += 64) {
+    const Stat x = s[c];
+    const float m = fmaxf(r.max, x.max);
+    r.sum = r.sum * ratio(r.max, m) + x.sum * ratio(x.max, m);
+    if (x.max > r.max || (x.max == r.max && x.idx < r.idx)) r.idx = x.idx;
+    r.max = m;
+  }
+  const float mine = r.max;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) fold_max(r.max, r.idx, o);
+  r.sum *= ratio(mine, r.max);
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) r.sum += __shfl_xor(r.sum, o);
+  return r;
+}
+
+// The accept tests of sequence b, its rows joined a wavefront each, then one
+// thread a draft; and (where `write`) the verdict and the outputs that follow:
+// all but the place of a token that is still to be drawn.
+template <typename T, bool PROBS>
+__device__ Verdict decide(const VerifyParams& p, int b, bool write) {
+  __shared__ int rejected_at;
+  __shared__ Stat p_rows[kMaxDrafts + 1], q_rows[kMaxDrafts];
+  const int n = drafts_of(p, b);
+  const float t = PROBS ? 1.f : temperature_of(p, b);
+  const int tid = threadIdx.x, places = p.a.drafts + 1;
+  const double inv_t = 1.0 / (t > 0.f ? t : 1.f);
+  if constexpr (!PROBS) {
+    const float scale = 1.44269504088896341f / (t > 0.f ? t : 1.f);
+    const int rows = n + 1 + (p.a.draft && t > 0.f ? n : 0);
+#pragma unroll 1
+    for (int r = tid >> 6; r < rows; r += kDrawWaves) {
+      const int64_t row = r <= n ? static_cast<int64_t>(b) * places + r
+                                 : static_cast<int64_t>(p.a.batch) * places + static_cast<int64_t>(b) * p.a.drafts +
+                                       (r - n - 1);
+      const Stat x = join_stats(p.stats + row * p.chunks, p.chunks, scale);
+      if ((tid & 63) == 0) (r <= n ? p_rows[r] : q_rows[r - n - 1]) = x;
+    }
+  }
+  if (tid == 0) rejected_at = n;
+  __syncthreads();
+  int d = -1;
+  double pd = 0.0;   // p of the draft
+  if (tid < n) {
+    const int64_t at = static_cast<int64_t>(b) * p.a.drafts + tid;
+    d = p.a.draft_tokens[at];
+    bool ok = false;
+    if (d >= 0 && d < p.a.vocab) {
+      double qd = 1.0;
+      int best = -1;
+      // p, then q where the draft has rows (a greedy sequence has no use for it)
+#pragma unroll 1
+      for (int k = 0; k < (p.a.draft && t > 0.f ? 2 : 1); ++k) {
+        const T x = (k ? draft_row<T>(p, b, tid) : target_row<T>(p, b, tid))[d];
+        double y;
+        if constexpr (PROBS) {
+          y = probability(widen<T>(x));
+        } else {
+          const Stat r = (k ? q_rows : p_rows)[tid];
+          y = r.sum > 0.0 ? weight(logit<T>(x), r.max, inv_t) / r.sum : 0.0;
+          if (k == 0) best = r.idx;
+        }
+        if (k) qd = y;
+        else pd = y;
+      }
+      ok = !PROBS && t == 0.f ? best == d : static_cast<double>(p.a.u_accept[at]) * qd < pd;
+    }
+    if (!ok) atomicMin(&rejected_at, tid);
+  }
+  __syncthreads();
+  const int accepted = rejected_at;
+  Verdict v{accepted, kFromP, -1, t > 0.f ? t : 1.f, 0.f, 0.f, {0, 0}};
+  int token = -1;
+  double token_p = 1.0;
+  if constexpr (!PROBS) {
+    const Stat r = p_rows[accepted];
+    v.p_max = r.max;
+    if (t == 0.f || r.max == -__builtin_inff()) {
+      v.how = kDone;
+      if (r.max > -__builtin_inff()) token = r.idx, token_p = 1.0 / r.sum;
+    }
+  }
+  if (accepted < n && v.how != kDone) {
+    if (p.a.draft) {
+      v.how = kFromRest;
+      if constexpr (!PROBS) v.q_max = q_rows[accepted].max;
+    } else {
+      v.skip = p.a.draft_tokens[static_cast<int64_t>(b) * p.a.drafts + accepted];
+    }
+  }
+  if (write && tid < places && (tid != accepted || v.how == kDone)) {
+    const int64_t at = static_cast<int64_t>(b) * places + tid;
+    p.a.tokens[at] = tid < accepted ? d : tid == accepted ? token : -1;
+    if (p.a.logprobs)
+      p.a.logprobs[at] = log_of(tid < accepted ? pd : tid == accepted ? token_p : 1.0);
+  }
+  if (write && tid == 0) {
+    p.a.accepted[b] = accepted;
+    p.verdicts[b] = v;
+  }
+  return v;
+}
+
+// Maximum and sum of exponentials of one chunk of one row, read in 16-byte
+// vectors from wherever the row begins: the chunks, and so the bits of the
+// result, do not depend on a row's place in memory.
 template <typename T>
-__global__ __launch_bounds__(kT) void verify_stats_kernel(const VerifyParams p, int target_rows) {
+__global__ __launch_bounds__(kT) void verify_rows_kernel(const VerifyParams p, int target_rows) {
   constexpr int kVec = 16 / sizeof(T), kLoads = kPer / kVec;
   __shared__ float wmax[kT / 64];
   __shared__ int widx[kT / 64];
   __shared__ double wsum[kT / 64];
   const int row = blockIdx.x / p.chunks, c = blockIdx.x - row * p.chunks;
-  int b, i;
-  const T* src;
   const bool is_target = row < target_rows;
-  if (is_target) {
-    b = row / (p.a.drafts + 1), i = row - b * (p.a.drafts + 1);
-    if (i > drafts_of(p, b)) return;
-    src = target_row<T>(p, b, i);
-  } else {
-    b = (row - target_rows) / p.a.drafts, i = (row - target_rows) - b * p.a.drafts;
-    if (i >= drafts_of(p, b) || temperature_of(p, b) == 0.f) return;
-    src = draft_row<T>(p, b, i);
-  }
+  const int b = is_target ? row / (p.a.drafts + 1) : (row - target_rows) / p.a.drafts;
+  const int i = is_target ? row - b * (p.a.drafts + 1) : row - target_rows - b * p.a.drafts;
+  const int n = drafts_of(p, b);
   const float t = temperature_of(p, b);
+  // (a greedy sequence does not use its draft's logits)
+  if (is_target ? i > n : i >= n || t == 0.f) return;
+  const T* src = is_target ? target_row<T>(p, b, i) : draft_row<T>(p, b, i);
   const float scale = 1.44269504088896341f / (t > 0.f ? t : 1.f);
-  const int lead = static_cast<int>(reinterpret_cast<uintptr_t>(src) / sizeof(T)) & (kVec - 1);
   float x[kPer];
   float m = -__builtin_inff();
   int idx = 0x7FFFFFFF;
 #pragma unroll
   for (int j = 0; j < kLoads; ++j) {
-    const int e0 = c * kChunk + (j * kT + threadIdx.x) * kVec - lead;
-    if (e0 >= 0 && e0 + kVec <= p.a.vocab) {
-      const u4 w = __builtin_nontemporal_load(reinterpret_cast<const u4*>(src + e0));
+    const int e0 = c * kChunk + (j * kT + threadIdx.x) * kVec;
+    if (e0 + kVec <= p.a.vocab) {
+      const u4 w = *reinterpret_cast<const u4_anywhere*>(src + e0);
 #pragma unroll
       for (int e = 0; e < kVec; ++e) {
         // (a cast of the vector element itself would read the vector's first)
@@ -159,7 +294,7 @@ __global__ __launch_bounds__(kT) void verify_stats_kernel(const VerifyParams p, 
     } else {
 #pragma unroll
       for (int e = 0; e < kVec; ++e)
-        x[j * kVec + e] = e0 + e >= 0 && e0 + e < p.a.vocab ? logit<T>(src[e0 + e]) : -__builtin_inff();
+        x[j * kVec + e] = e0 + e < p.a.vocab ? logit<T>(src[e0 + e]) : -__builtin_inff();
     }
 #pragma unroll
     for (int e = 0; e < kVec; ++e)
@@ -192,327 +327,260 @@ __global__ __launch_bounds__(kT) void verify_stats_kernel(const VerifyParams p, 
   }
 }
 
-// One row's chunks as one, by a wavefront (all lanes return it).
-__device__ __forceinline__ Stat join_stats(const Stat* s, int chunks, float t) {
-  const int lane = threadIdx.x & 63;
-  const double inv_t = 1.0 / (t > 0.f ? t : 1.f);
-  Stat r{-__builtin_inff(), 0x7FFFFFFF, 0.0};
-  for (int c = lane; c < chunks; c += 64) {
-    const Stat x = s[c];
-    if (x.max > r.max || (x.max == r.max && x.idx < r.idx)) r.max = x.max, r.idx = x.idx;
-  }
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) fold_max(r.max, r.idx, o);
-  for (int c = lane; c < chunks; c += 64) r.sum += s[c].sum * weight(s[c].max, r.max, inv_t);
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) r.sum += __shfl_xor(r.sum, o);
-  return r;
-}
-
-// What the accept tests say of a sequence.
-struct Verdict {
-  int accepted, n;
-  float t;             // 0: greedy
-  float p_max, q_max;  // maxima of the rows that the token is picked from
-  int best;            // the target row's largest logit
-  double p_sum;        // 32-bit precise
-};
-
-struct VerdictShared {
-  int ok[kMaxDrafts + 1];
-  float pmax[kMaxDrafts + 1], qmax[kMaxDrafts + 1];
-  int best[kMaxDrafts + 1];
-  double psum[kMaxDrafts + 1];
-};
-
-template <typename T, bool PROBS>
-__device__ Verdict decide(const VerifyParams& p, int b, VerdictShared& sh) {
-  const int n = drafts_of(p, b), wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const float t = temperature_of(p, b);
-  const double inv_t = 1.0 / (t > 0.f ? t : 1.f);
-  for (int i = wave; i <= n; i += kT / 64) {
-    const int d = i < n ? p.a.draft_tokens[static_cast<int64_t>(b) * p.a.drafts + i] : 0;
-    const bool known = d >= 0 && d < p.a.vocab;
-    const T* pr = target_row<T>(p, b, i);
-    bool ok = false;
-    Stat ps{0.f, 0, 0.0}, qs{0.f, 0, 0.0};
-    if constexpr (PROBS) {
-      if (i < n && known) {
-        const double pd = probability(widen<T>(pr[d]));
-        const double qd = p.a.draft ? probability(widen<T>(draft_row<T>(p, b, i)[d])) : 1.0;
-        ok = static_cast<double>(p.a.u_accept[static_cast<int64_t>(b) * p.a.drafts + i]) * qd < pd;
-      }
-    } else {
-      ps = join_stats(p.stats + (static_cast<int64_t>(b) * (p.a.drafts + 1) + i) * p.chunks, p.chunks, t);
-      if (i < n && t == 0.f) {
-        ok = known && ps.idx == d;
-      } else if (i < n) {
-        if (p.a.draft)
-          qs = join_stats(p.stats + (static_cast<int64_t>(p.a.batch) * (p.a.drafts + 1) +
-                                     static_cast<int64_t>(b) * p.a.drafts + i) * p.chunks, p.chunks, t);
-        if (known) {
-          const double pd = ps.sum > 0.0 ? weight(logit<T>(pr[d]), ps.max, inv_t) / ps.sum : 0.0;
-          double qd = 1.0;
-          if (p.a.draft) qd = qs.sum > 0.0 ? weight(logit<T>(draft_row<T>(p, b, i)[d]), qs.max, inv_t) / qs.sum : 0.0;
-          ok = static_cast<double>(p.a.u_accept[static_cast<int64_t>(b) * p.a.drafts + i]) * qd < pd;
-        }
-      }
-    }
-    if (lane == 0) {
-      sh.ok[i] = ok;
-      sh.pmax[i] = ps.max, sh.qmax[i] = qs.max;
-      sh.best[i] = ps.idx;
-      sh.psum[i] = ps.sum;
-    }
-  }
-  __syncthreads();
-  int a = 0;
-  while (a < n && sh.ok[a]) ++a;
-  return Verdict{a, n, t, sh.pmax[a], sh.qmax[a], sh.best[a], sh.psum[a]};
-}
-
-// The unnormalized weights of place `e` of the row the token is picked from:
-// of p (without the rejected draft `skip`, where no draft row is given) and of q.
-template <typename T, bool PROBS>
-__device__ __forceinline__ double p_weight(const T* row, int e, float max, double inv_t, int skip) {
-  if (e == skip) return 0.0;
-  if constexpr (PROBS)
-    return probability(widen<T>(row[e]));
-  else
-    return weight(logit<T>(row[e]), max, inv_t);
-}
-
-// Sums over a chunk of up to two quantities, to thread 0.
-__device__ __forceinline__ void block_sum2(double& a, double& b, double (*buf)[2]) {
-#pragma unroll
+// Two sums over the workgroup, to every thread.
+__device__ __forceinline__ void block_sum2(double& a, double& b, double (&buf)[kDrawWaves][2]) {
+#pragma unroll 1
   for (int o = 1; o < 64; o <<= 1) a += __shfl_xor(a, o), b += __shfl_xor(b, o);
   if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6][0] = a, buf[threadIdx.x >> 6][1] = b;
   __syncthreads();
   a = b = 0.0;
-#pragma unroll
-  for (int w = 0; w < kT / 64; ++w) a += buf[w][0], b += buf[w][1];
-}
-
-// LEFT false: the chunk's sums of p and of q (and, of probabilities, of what
-// q leaves over at once); true: of what q leaves over.
-template <typename T, bool PROBS, bool LEFT>
-__global__ __launch_bounds__(kT) void verify_sums_kernel(const VerifyParams p) {
-  __shared__ VerdictShared sh;
-  __shared__ double buf[kT / 64][2];
-  const int b = blockIdx.x / p.chunks, c = blockIdx.x - b * p.chunks;
-  const Verdict v = decide<T, PROBS>(p, b, sh);
-  const bool rejected = v.accepted < v.n;
-  if constexpr (!PROBS)
-    if (v.t == 0.f) return;  // greedy: nothing is drawn
-  const bool with_q = rejected && p.a.draft;
-  if (LEFT && !with_q) return;
-  const double inv_t = 1.0 / (v.t > 0.f ? v.t : 1.f);
-  const T* pr = target_row<T>(p, b, v.accepted);
-  const T* qr = with_q ? draft_row<T>(p, b, v.accepted) : nullptr;
-  const int skip =
-      rejected && !p.a.draft ? p.a.draft_tokens[static_cast<int64_t>(b) * p.a.drafts + v.accepted] : -1;
-  double* sums = p.sums + static_cast<int64_t>(b) * 3 * p.chunks;
-  double inv_p = 0.0, inv_q = 0.0;
-  if constexpr (LEFT) {
-    double zp = 0.0, zq = 0.0;
-    for (int j = threadIdx.x; j < p.chunks; j += kT) zp += sums[j], zq += sums[p.chunks + j];
-    block_sum2(zp, zq, buf);
-    inv_p = zp > 0.0 ? 1.0 / zp : 0.0;
-    inv_q = zq > 0.0 ? 1.0 / zq : 0.0;
-    __syncthreads();
-  }
-  double sp = 0.0, sq = 0.0;
 #pragma unroll 4
-  for (int j = 0; j < kPer; ++j) {
-    const int e = c * kChunk + j * kT + threadIdx.x;
-    if (e >= p.a.vocab) break;
-    const double wp = p_weight<T, PROBS>(pr, e, v.p_max, inv_t, skip);
-    const double wq = with_q ? p_weight<T, PROBS>(qr, e, v.q_max, inv_t, -1) : 0.0;
-    if constexpr (LEFT) {
-      sp += fmax(wp * inv_p - wq * inv_q, 0.0);
-    } else if constexpr (PROBS) {
-      sp += wp;
-      sq += fmax(wp - wq, 0.0);
-    } else {
-      sp += wp;
-      sq += wq;
-    }
-  }
-  block_sum2(sp, sq, buf);
-  if (threadIdx.x == 0) {
-    if constexpr (LEFT) {
-      sums[2 * p.chunks + c] = sp;
-    } else if constexpr (PROBS) {
-      sums[c] = sp;
-      sums[2 * p.chunks + c] = sq;
-    } else {
-      sums[c] = sp;
-      sums[p.chunks + c] = sq;
-    }
-  }
+  for (int w = 0; w < kDrawWaves; ++w) a += buf[w][0], b += buf[w][1];
 }
 
-// Inclusive running sum over the workgroup's threads, in thread order.
-__device__ __forceinline__ double block_scan(double x, double* wsum) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
+// Inclusive running sum over a wavefront's lanes.
+__device__ __forceinline__ double wave_scan(double x) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll 1
   for (int o = 1; o < 64; o <<= 1) {
     const double y = __shfl_up(x, o);
     if (lane >= o) x += y;
   }
-  __syncthreads();
-  if (lane == 63) wsum[wave] = x;
-  __syncthreads();
-  for (int w = 0; w < wave; ++w) x += wsum[w];
   return x;
 }
 
-// One workgroup a sequence: the token and the outputs.
-template <typename T, bool PROBS>
-__global__ __launch_bounds__(kT) void verify_pick_kernel(const VerifyParams p) {
-  __shared__ VerdictShared sh;
-  __shared__ double wsum[kT / 64];
-  __shared__ double buf[kT / 64][2];
-  __shared__ int found, last;
-  __shared__ double before;
-  const int b = blockIdx.x, tid = threadIdx.x;
-  const Verdict v = decide<T, PROBS>(p, b, sh);
-  const bool rejected = v.accepted < v.n, greedy = !PROBS && v.t == 0.f;
-  const double inv_t = 1.0 / (v.t > 0.f ? v.t : 1.f);
+// The weights of this thread's places e0 + j * step of the row that a token is
+// drawn from: of p without the struck draft, and of q where qr is given.
+// SMALL: with one copy of the exponential, for a kernel of few workgroups.
+template <typename T, bool PROBS, bool SMALL>
+__device__ __forceinline__ void weights(const VerifyParams& p, const Verdict& v, const T* pr, const T* qr, int e0,
+                                        int step, double (&wp)[kDrawPer], double (&wq)[kDrawPer]) {
+  float x[kDrawPer], y[kDrawPer];
+#pragma unroll
+  for (int j = 0; j < kDrawPer; ++j) {
+    const int e = e0 + j * step;
+    const bool in = e < p.a.vocab;
+    if constexpr (PROBS) {
+      wp[j] = in && e != v.skip ? probability(widen<T>(pr[e])) : 0.0;
+      wq[j] = in && qr ? probability(widen<T>(qr[e])) : 0.0;
+    } else {
+      x[j] = in && e != v.skip ? logit<T>(pr[e]) : -__builtin_inff();
+      y[j] = in && qr ? logit<T>(qr[e]) : -__builtin_inff();
+    }
+  }
+  if constexpr (!PROBS) {
+    static_assert(kDrawPer == 4, "four places are told apart below");
+    const double inv_t = 1.0 / v.t;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) wq[j] = 0.0;
+    if constexpr (SMALL) {
+#pragma unroll 1
+      for (int k = 0; k < (qr ? 8 : 4); ++k) {
+        const int j = k & 3;
+        const float xs = j == 0 ? x[0] : j == 1 ? x[1] : j == 2 ? x[2] : x[3];
+        const float ys = j == 0 ? y[0] : j == 1 ? y[1] : j == 2 ? y[2] : y[3];
+        const double w = weight(k < 4 ? xs : ys, k < 4 ? v.p_max : v.q_max, inv_t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (k == i) wp[i] = w;
+          if (k == 4 + i) wq[i] = w;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) wp[j] = weight(x[j], v.p_max, inv_t);
+      if (qr) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) wq[j] = weight(y[j], v.q_max, inv_t);
+      }
+    }
+  }
+}
+
+// The accept tests alone, a workgroup a sequence.
+template <typename T>
+__global__ __launch_bounds__(kD) void verify_decide_kernel(const VerifyParams p) {
+  decide<T, false>(p, blockIdx.x, true);
+}
+
+// Chunk sums of the row that a token is picked from. REST false: of p and,
+// where its draft was rejected, of q; of probabilities, which need no totals,
+// also of what q leaves over. REST true: of what q leaves over.
+template <typename T, bool PROBS, bool REST>
+__global__ __launch_bounds__(kD) void verify_sums_kernel(const VerifyParams p) {
+  __shared__ double buf[kDrawWaves][2];
+  const int b = blockIdx.x / p.chunks, c = blockIdx.x - b * p.chunks;
+  const Verdict v = REST || p.decided ? p.verdicts[b] : decide<T, PROBS>(p, b, c == 0);
+  if (v.how == kDone || (REST && v.how != kFromRest)) return;
   const T* pr = target_row<T>(p, b, v.accepted);
-  int token = -1;
-  if (greedy) {
-    if (v.p_max > -__builtin_inff()) token = v.best;
-  } else {
-    const int32_t d = rejected ? p.a.draft_tokens[static_cast<int64_t>(b) * p.a.drafts + v.accepted] : -1;
-    int skip = rejected && !p.a.draft ? d : -1;
-    bool with_q = rejected && p.a.draft;
-    const T* qr = with_q ? draft_row<T>(p, b, v.accepted) : nullptr;
-    const double* sums = p.sums + static_cast<int64_t>(b) * 3 * p.chunks;
-    // the totals of p, q and of what is left over
-    double zp = 0.0, zq = 0.0, zl = 0.0, none = 0.0;
-    for (int j = tid; j < p.chunks; j += kT) {
-      zp += sums[j];
-      if (with_q) {
-        if constexpr (!PROBS) zq += sums[p.chunks + j];
-        zl += sums[2 * p.chunks + j];
-      }
-    }
+  const T* qr = v.how == kFromRest ? draft_row<T>(p, b, v.accepted) : nullptr;
+  double* sums = p.sums + static_cast<int64_t>(b) * 3 * p.chunks;
+  double wp[kDrawPer], wq[kDrawPer];
+  weights<T, PROBS, false>(p, v, pr, qr, c * kChunk + threadIdx.x, kD, wp, wq);
+  double scale_p = 1.0, scale_q = 1.0;
+  if constexpr (REST) {
+    double zp = 0.0, zq = 0.0;
+#pragma unroll 1
+    for (int j = threadIdx.x; j < p.chunks; j += kD) zp += sums[j], zq += sums[p.chunks + j];
     block_sum2(zp, zq, buf);
+    scale_p = zp > 0.0 ? 1.0 / zp : 0.0;
+    scale_q = zq > 0.0 ? 1.0 / zq : 0.0;
     __syncthreads();
-    block_sum2(zl, none, buf);
-    const double inv_p = PROBS ? 1.0 : (zp > 0.0 ? 1.0 / zp : 0.0), inv_q = PROBS ? 1.0 : (zq > 0.0 ? 1.0 / zq : 0.0);
-    double total = with_q ? zl : zp;
-    bool rest_of_p = false;  // nothing is left over: from p
-    if (!(total > 0.0) && rejected) {
-      if (with_q) {
-        with_q = false;
-        total = zp;
-      } else {
-        // p without the draft is nothing: the draft is all there is
-        rest_of_p = true;
-        skip = -1;
-      }
-    }
-    if (rest_of_p) {
-      const bool known = d >= 0 && d < p.a.vocab;
-      if (tid == 0 && known && p_weight<T, PROBS>(pr, d, v.p_max, inv_t, -1) > 0.0) found = d;
-      else if (tid == 0) found = -1;
-      __syncthreads();
-      token = found;
-    } else if (total > 0.0) {
-      const double* cs = with_q ? sums + 2 * p.chunks : sums;
-      const double aim = static_cast<double>(p.a.u_sample[b]) * total;
-      // the first chunk whose running sum exceeds the aim (or the last that holds anything)
-      if (tid == 0) found = 0x7FFFFFFF, last = -1;
-      __syncthreads();
-      double run = 0.0;
-      for (int j0 = 0; j0 < p.chunks; j0 += kT) {
-        const int j = j0 + tid;
-        const double x = j < p.chunks ? cs[j] : 0.0;
-        const double sum = run + block_scan(x, wsum);
-        if (j < p.chunks && x > 0.0) {
-          if (sum > aim) atomicMin(&found, j);
-          atomicMax(&last, j);
-        }
-        __syncthreads();
-        if (found == j) before = sum - x;
-        run += wsum[0] + wsum[1] + wsum[2] + wsum[3];
-        __syncthreads();
-        if (found != 0x7FFFFFFF) break;
-      }
-      const bool whole = found == 0x7FFFFFFF;  // rounding: past the end, the last token that counts
-      const int c = whole ? last : found;
-      const double left = whole ? __builtin_inf() : aim - before;
-      __syncthreads();
-      if (tid == 0) found = 0x7FFFFFFF, last = -1;
-      double w[kPer], mine = 0.0;
+  }
+  double sp = 0.0, sq = 0.0;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int e = c * kChunk + tid * kPer + j;
-        w[j] = 0.0;
-        if (e < p.a.vocab) {
-          w[j] = p_weight<T, PROBS>(pr, e, v.p_max, inv_t, skip);
-          if (with_q) w[j] = fmax(w[j] * inv_p - p_weight<T, PROBS>(qr, e, v.q_max, inv_t, -1) * inv_q, 0.0);
-        }
-        mine += w[j];
-      }
-      double sum = block_scan(mine, wsum) - mine;
-      int hit = 0x7FFFFFFF, end = -1;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        sum += w[j];
-        if (w[j] > 0.0) {
-          end = c * kChunk + tid * kPer + j;
-          if (sum > left && hit == 0x7FFFFFFF) hit = end;
-        }
-      }
-      if (hit != 0x7FFFFFFF) atomicMin(&found, hit);
-      if (end >= 0) atomicMax(&last, end);
-      __syncthreads();
-      token = found != 0x7FFFFFFF ? found : last;
+  for (int j = 0; j < kDrawPer; ++j) {
+    if constexpr (REST) {
+      sp += fmax(wp[j] * scale_p - wq[j] * scale_q, 0.0);
+    } else {
+      sp += wp[j];
+      sq += PROBS ? fmax(wp[j] - wq[j], 0.0) : wq[j];
     }
   }
-  // outputs: place tid
-  const int places = p.a.drafts + 1;
-  if (tid < places) {
-    int out = -1;
-    if (tid < v.accepted) out = p.a.draft_tokens[static_cast<int64_t>(b) * p.a.drafts + tid];
-    else if (tid == v.accepted) out = token;
-    p.a.tokens[static_cast<int64_t>(b) * places + tid] = out;
-    if (p.a.logprobs) {
-      double lp = 0.0;
-      if (out >= 0) {
-        const T x = target_row<T>(p, b, tid)[out];
-        if constexpr (PROBS) {
-          lp = log(probability(widen<T>(x)));
-        } else {
-          const float y = logit<T>(x);
-          lp = (y == sh.pmax[tid] ? 0.0 : (static_cast<double>(y) - static_cast<double>(sh.pmax[tid])) * inv_t) -
-               log(sh.psum[tid]);
-        }
-      }
-      p.a.logprobs[static_cast<int64_t>(b) * places + tid] = static_cast<float>(lp);
+  block_sum2(sp, sq, buf);
+  if (threadIdx.x == 0) {
+    if constexpr (REST) {
+      sums[2 * p.chunks + c] = sp;
+    } else {
+      sums[c] = sp;
+      sums[(PROBS ? 2 : 1) * p.chunks + c] = sq;
     }
   }
-  if (tid == 0) p.a.accepted[b] = v.accepted;
+}
+
+// The token that u_sample picks, one workgroup a sequence: from max(p - q, 0)
+// for a rejected draft with a row, else from p (without v.skip). The first
+// wavefront finds the chunk, then all of them its token.
+template <typename T, bool PROBS>
+__global__ __launch_bounds__(kD) void verify_pick_kernel(const VerifyParams p) {
+  __shared__ double w[kChunk];
+  __shared__ double wsum[kDrawWaves];
+  __shared__ double s_left, s_scale_p, s_scale_q, s_zp;
+  __shared__ int s_chunk, s_rest, found, last;
+  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const Verdict v = p.verdicts[b];
+  if (v.how == kDone) return;
+  const T* pr = target_row<T>(p, b, v.accepted);
+  const T* qr = v.how == kFromRest ? draft_row<T>(p, b, v.accepted) : nullptr;
+  if (wave == 0) {
+    const double* sums = p.sums + static_cast<int64_t>(b) * 3 * p.chunks;
+    const float u = p.a.u_sample[b];
+    // the totals of p, q and of what is left over
+    double z[3] = {0.0, 0.0, 0.0};
+#pragma unroll 1
+    for (int j = lane; j < p.chunks; j += 64) {
+      z[0] += sums[j];
+      if (qr) {
+        if constexpr (!PROBS) z[1] += sums[p.chunks + j];
+        z[2] += sums[2 * p.chunks + j];
+      }
+    }
+#pragma unroll 1
+    for (int o = 1; o < 64; o <<= 1)
+#pragma unroll
+      for (int k = 0; k < 3; ++k) z[k] += __shfl_xor(z[k], o);
+    const bool rest = qr && z[2] > 0.0;  // nothing left over: from p
+    const double* cs = rest ? sums + 2 * p.chunks : sums;
+    const double aim = static_cast<double>(u) * (rest ? z[2] : z[0]);
+    // the first chunk whose running sum exceeds the aim; by rounding there may
+    // be none: then the last that holds anything, and all of it
+    int chunk = -1;
+    double run = 0.0, before = -__builtin_inf();
+#pragma unroll 1
+    for (int j0 = 0; j0 < p.chunks; j0 += 64) {
+      const double x = j0 + lane < p.chunks ? cs[j0 + lane] : 0.0;
+      const double sum = run + wave_scan(x);
+      const unsigned long long over = __ballot(x > 0.0 && sum > aim), some = __ballot(x > 0.0);
+      if (over) {
+        const int l = __builtin_ctzll(over);
+        chunk = j0 + l;
+        before = __shfl(sum - x, l);
+        break;
+      }
+      if (some) chunk = j0 + 63 - __builtin_clzll(some);
+      run = __shfl(sum, 63);
+    }
+    if (lane == 0) {
+      s_chunk = chunk;
+      s_left = aim - before;
+      s_rest = rest;
+      s_zp = z[0];
+      s_scale_p = !PROBS && rest ? 1.0 / z[0] : 1.0;
+      s_scale_q = !PROBS && rest && z[1] > 0.0 ? 1.0 / z[1] : PROBS && rest ? 1.0 : 0.0;
+      found = 0x7FFFFFFF, last = -1;
+    }
+  }
+  __syncthreads();
+  int token = -1;
+  const int chunk = s_chunk;
+  if (chunk >= 0) {
+    double wp[kDrawPer], wq[kDrawPer];
+    weights<T, PROBS, true>(p, v, pr, s_rest ? qr : nullptr, chunk * kChunk + tid, kD, wp, wq);
+#pragma unroll
+    for (int j = 0; j < kDrawPer; ++j) w[j * kD + tid] = fmax(wp[j] * s_scale_p - wq[j] * s_scale_q, 0.0);
+    __syncthreads();
+    double mine = 0.0;
+#pragma unroll
+    for (int j = 0; j < kDrawPer; ++j) mine += w[tid * kDrawPer + j];
+    double sum = wave_scan(mine);
+    if (lane == 63) wsum[wave] = sum;
+    __syncthreads();
+    sum -= mine;
+#pragma unroll 1
+    for (int k = 0; k < wave; ++k) sum += wsum[k];
+    int hit = 0x7FFFFFFF, end = -1;
+#pragma unroll
+    for (int j = 0; j < kDrawPer; ++j) {
+      const double x = w[tid * kDrawPer + j];
+      sum += x;
+      if (x > 0.0) {
+        end = tid * kDrawPer + j;
+        if (sum > s_left && hit == 0x7FFFFFFF) hit = end;
+      }
+    }
+    if (hit != 0x7FFFFFFF) atomicMin(&found, hit);
+    if (end >= 0) atomicMax(&last, end);
+    __syncthreads();
+    token = chunk * kChunk + (found != 0x7FFFFFFF ? found : last);
+  }
+  if (tid < 2) {
+    // lane 0: the token's weight in p; lane 1: that of the struck draft, which is in no sum
+    const int e = tid == 0 ? token : v.skip;
+    double x = 0.0;
+    if (e >= 0 && e < p.a.vocab) {
+      if constexpr (PROBS) x = probability(widen<T>(pr[e]));
+      else x = weight(logit<T>(pr[e]), v.p_max, 1.0 / v.t);
+    }
+    const double struck = __shfl_xor(x, 1);
+    if (tid == 0) {
+      if (token < 0 && struck > 0.0) token = v.skip, x = struck;  // it is all that p is
+      const int64_t at = static_cast<int64_t>(b) * (p.a.drafts + 1) + v.accepted;
+      p.a.tokens[at] = token;
+      if (p.a.logprobs) p.a.logprobs[at] = log_of(token < 0 ? 1.0 : PROBS ? x : x / (s_zp + struck));
+    }
+  }
 }
 
 template <typename T>
 hipError_t launch_logits(const VerifyParams& p, hipStream_t stream) {
   const int target_rows = p.a.batch * (p.a.drafts + 1);
-  const int rows = target_rows + (p.a.draft ? p.a.batch * p.a.drafts : 0);
-  verify_stats_kernel<T><<<dim3(static_cast<uint32_t>(rows) * p.chunks), kT, 0, stream>>>(p, target_rows);
+  const bool with_draft = p.a.draft && p.a.drafts > 0;
+  const int rows = target_rows + (with_draft ? p.a.batch * p.a.drafts : 0);
+  verify_rows_kernel<T><<<dim3(static_cast<uint32_t>(rows) * p.chunks), kT, 0, stream>>>(p, target_rows);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const dim3 grid(static_cast<uint32_t>(p.a.batch) * p.chunks);
-  verify_sums_kernel<T, false, false><<<grid, kT, 0, stream>>>(p);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  if (p.a.draft && p.a.drafts > 0) {
-    verify_sums_kernel<T, false, true><<<grid, kT, 0, stream>>>(p);
+  if (p.decided) {
+    verify_decide_kernel<T><<<dim3(p.a.batch), kD, 0, stream>>>(p);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  verify_pick_kernel<T, false><<<dim3(p.a.batch), kT, 0, stream>>>(p);
+  verify_sums_kernel<T, false, false><<<grid, kD, 0, stream>>>(p);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (with_draft) {
+    verify_sums_kernel<T, false, true><<<grid, kD, 0, stream>>>(p);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  verify_pick_kernel<T, false><<<dim3(p.a.batch), kD, 0, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -522,13 +590,19 @@ hipError_t launch_verify(const qpn_verify_args& a, const VerifyPlan& plan, void*
   VerifyParams p;
   p.a = a;
   p.chunks = plan.chunks;
-  p.stats = static_cast<Stat*>(workspace);
-  p.sums = reinterpret_cast<double*>(static_cast<uint8_t*>(workspace) + plan.stat_bytes);
+  // Up to one workgroup a slot (two a compute unit) each makes its sequence's
+  // accept tests itself, beyond that a launch of their own makes them once: 8
+  // rows 9.5 us against 7 + 5, 480 rows 36 us against 8 + 14.
+  p.decided = !a.probabilities && a.batch * plan.chunks > 2 * kComputeUnits;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.verdicts = reinterpret_cast<Verdict*>(ws);
+  p.stats = reinterpret_cast<Stat*>(ws += plan.verdict_bytes);
+  p.sums = reinterpret_cast<double*>(ws + plan.stat_bytes);
   if (a.probabilities) {
-    verify_sums_kernel<float, true, false><<<dim3(static_cast<uint32_t>(a.batch) * p.chunks), kT, 0, stream>>>(p);
+    verify_sums_kernel<float, true, false><<<dim3(static_cast<uint32_t>(a.batch) * p.chunks), kD, 0, stream>>>(p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    verify_pick_kernel<float, true><<<dim3(a.batch), kT, 0, stream>>>(p);
+    verify_pick_kernel<float, true><<<dim3(a.batch), kD, 0, stream>>>(p);
     return hipGetLastError();
   }
   switch (a.dtype) {

@@ -107,9 +107,9 @@ qpn_status plan_attention(const qpn_kv4_cache* c, const qpn_kv4_attention_args* 
   if (static_cast<int64_t>(a->rows) * a->heads > kMaxGroups) return QPN_ERR_UNSUPPORTED;
   p->groups = a->max_kv_len <= kWholeRunTokens ? 0 : kComputeUnits * attn_waves_per_simd(c->head_dim, p->tiles16);
   p->min_share = kAttnWaves;
-  p->sched_bytes = (static_cast<size_t>(a->batch) + 1) * 16;
+  p->cut_bytes = static_cast<size_t>(p->groups) * 32;
   p->partial_bytes = 2 * static_cast<size_t>(p->groups) * 16 * p->tiles16 * (c->head_dim + 2) * sizeof(float);
-  p->total_bytes = a->batch == 0 || a->rows == 0 || p->groups == 0 ? 0 : p->sched_bytes + p->partial_bytes;
+  p->total_bytes = a->batch == 0 || a->rows == 0 || p->groups == 0 ? 0 : p->cut_bytes + p->partial_bytes;
   return QPN_OK;
 }
 

@@ -23,7 +23,7 @@ struct AttentionPlan {
   int row_tiles;  // a sequence's row tiles, at most
   int groups;     // workgroups that share the tiles evenly; 0: a workgroup a run, no join
   int min_share;  // tiles a workgroup takes at least
-  size_t sched_bytes, partial_bytes, total_bytes;
+  size_t cut_bytes, partial_bytes, total_bytes;
 };
 
 int64_t kv4_segment_bytes(int page_size, int head_dim);

@@ -52,9 +52,17 @@ struct AttnParams {
   const int32_t* q_start;
   int32_t batch, rows, max_q, max_kv, window, row_tiles, groups, min_share, q_aligned;
   float f, v_scale;  // f: scale * log2(e) * k_scale
-  int4* sched;       // [batch]: where the sequence's tiles begin, their number, row tiles; then [1]: the share
-  float* part;       // [2 groups][16 NQ][DIM], then [2 groups][16 NQ][2]; groups 0: no join
+  struct Cut* cuts;  // [groups]; groups 0: no join
+  float* part;       // [2 groups][16 NQ][DIM], then [2 groups][16 NQ][2]
 };
+
+// The run that a workgroup's share begins inside of (rows 0: it begins with
+// one): its pieces are those of workgroups first .. last, its rows `rows` of
+// kv head `head`'s from row `row0` of the sequence whose rows begin at `qs`.
+struct Cut {
+  int rows, first, last, qs, row0, head, pad[2];
+};
+static_assert(sizeof(Cut) == 32, "the workspace holds 32 bytes a workgroup");
 
 // One sequence's share of the work.
 struct Seq {
@@ -77,6 +85,12 @@ __device__ __forceinline__ Seq sequence(const AttnParams& a, int b, int rows_per
   s.tiles = max(1, (s.len + kTileTokens - 1) / kTileTokens - s.lo);  // an empty sequence is one tile that holds nothing
   s.rt = (s.ql * a.group + rows_per_tile - 1) / rows_per_tile;
   return s;
+}
+
+// Lane l's sequence, in scalar registers.
+__device__ __forceinline__ Seq lane_of(const Seq& s, int l) {
+  const auto get = [&](int x) { return __builtin_amdgcn_readlane(x, l); };
+  return Seq{get(s.len), get(s.qs), get(s.ql), get(s.lo), get(s.tiles), get(s.rt)};
 }
 
 // The codes and scales of 32 tokens as a lane holds them.
@@ -298,23 +312,25 @@ __global__ __launch_bounds__(kW * 64, attn_waves_per_simd(DIM, NQ)) void kv4_att
   const AttnParams& a0 = params;
   // This workgroup's share [at, end) of the line, and the sequence b, whose
   // tiles begin at `base`, that the share begins in.
-  int b = 0, base = 0, at, end;
+  int b = 0, base = 0, at, end, share = 0;
+  Seq seq = {0, 0, 0, 0, 0, 0};
   if (a0.groups == 0) {
     const int per = a0.row_tiles * a0.kv_heads;
     b = group_id / per;
-    const Seq s = sequence(a0, b, kRows);
-
-    at = (group_id - b * per) * (s.tiles + kRunCost);
-    end = at + s.tiles + kRunCost;
-    if (at >= s.rt * a0.kv_heads * (s.tiles + kRunCost)) return;  // the sequence has fewer row tiles than the longest
+    seq = sequence(a0, b, kRows);
+    at = (group_id - b * per) * (seq.tiles + kRunCost);
+    end = at + seq.tiles + kRunCost;
+    if (at >= seq.rt * a0.kv_heads * (seq.tiles + kRunCost)) return;  // the sequence has fewer row tiles than the longest
   } else {
     int total = 0;
-    int mine = 0, sum = 0;  // of the last 64 sequences: a lane's tiles, and their running sum
+    // of the last 64 sequences: a lane's, its part of the line, and the running sum
+    Seq lanes = {0, 0, 0, 0, 0, 0};
+    int mine = 0, sum = 0;
     const auto count = [&](int b0) {
       mine = 0;
       if (b0 + lane < a0.batch) {
-        const Seq s = sequence(a0, b0 + lane, kRows);
-        mine = (s.tiles + kRunCost) * s.rt * a0.kv_heads;
+        lanes = sequence(a0, b0 + lane, kRows);
+        mine = (lanes.tiles + kRunCost) * lanes.rt * a0.kv_heads;
       }
       sum = mine;
 #pragma unroll
@@ -327,13 +343,14 @@ __global__ __launch_bounds__(kW * 64, attn_waves_per_simd(DIM, NQ)) void kv4_att
       count(b0);
       total += __builtin_amdgcn_readlane(sum, 63);
     }
-    const int share = max(a0.min_share, (total + a0.groups - 1) / a0.groups);
-    if (group_id == 0 && tid == 0) a0.sched[a0.batch] = int4{share, 0, 0, 0};
+    share = max(a0.min_share, (total + a0.groups - 1) / a0.groups);
     at = group_id * share;  // groups * share is at most 2^31 - 1, as the line is
     end = min(at + share, total);
-    if (at >= total) return;
+    if (at >= total) {
+      if (tid == 0) a0.cuts[group_id].rows = 0;
+      return;
+    }
     int before = 0;
-
     for (int b0 = 0; b0 < a0.batch; b0 += 64) {
       if (a0.batch > 64) count(b0);
       const int all = __builtin_amdgcn_readlane(sum, 63);
@@ -341,11 +358,13 @@ __global__ __launch_bounds__(kW * 64, attn_waves_per_simd(DIM, NQ)) void kv4_att
         const int l = __builtin_ctzll(__ballot(at < before + sum));
         b = b0 + l;
         base = before + __builtin_amdgcn_readlane(sum, l) - __builtin_amdgcn_readlane(mine, l);
+        seq = lane_of(lanes, l);
         break;
       }
       before += all;
     }
   }
+  bool first_run = true;
   while (true) {
   // (what follows from the lane is worked out again for every run: kept from
   // one to the next it would take registers that the occupancy needs;
@@ -353,18 +372,23 @@ __global__ __launch_bounds__(kW * 64, attn_waves_per_simd(DIM, NQ)) void kv4_att
   asm volatile("" : "+v"(tid), "+v"(lane));
   const AttnParams& a = reread(params);
   const int i = lane & 15, g = lane >> 4;
-  const Seq s = sequence(a, b, kRows);
+  const Seq s = seq;
   const int cost = s.tiles + kRunCost;
   const int run = (at - base) / cost, from = at - base - run * cost, to = min(cost, from + end - at);
   const int tile0 = max(0, from - kRunCost), tiles = max(0, to - kRunCost) - tile0;
   at += to - from;
   const int rtile = run / a.kv_heads, head = run - rtile * a.kv_heads;
   const bool alone = tiles == s.tiles;  // the whole run
-  if (a.groups && run == 0 && from == 0 && tid == 0) a.sched[b] = int4{base, s.tiles, 0, 0};
-  if (tiles > 0) {
-
   // The rows: row r of the row tile is query row r / group, head r % group.
   const int row0 = rtile * kRows, nrows = min(s.ql * a.group - row0, kRows);
+  if (first_run && a.groups && tid == 0) {
+    // where this run's first tile and its last lie on the line
+    const int begin = base + run * cost + kRunCost;
+    a.cuts[group_id] = Cut{tile0 > 0 ? nrows : 0, begin / share, (begin + s.tiles - 1) / share, s.qs, row0, head, {0, 0}};
+  }
+  first_run = false;
+  if (tiles > 0) {
+
   h8 qreg[kQueriesInLds ? 1 : NQ][kSteps];
   float f[NQ], m[NQ], l[NQ];
   f4 o[NQ][kBlocks];
@@ -721,79 +745,68 @@ __global__ __launch_bounds__(kW * 64, attn_waves_per_simd(DIM, NQ)) void kv4_att
   if (at - base >= cost * s.rt * reread(params).kv_heads) {
     // the next sequence that has rows
     base = at;
-    do ++b;
-    while (sequence(reread(params), b, kRows).rt == 0);
+    do seq = sequence(reread(params), ++b, kRows);
+    while (seq.rt == 0);
   }
   }
 }
 
-// Joins the pieces of the runs that were cut: one wavefront a (row, query
-// head), the pieces in the order of the line.
-template <int DIM, bool BF16>
-__global__ __launch_bounds__(256) void kv4_attention_join_kernel(const AttnParams a, int unit_rows) {
+// Joins the pieces of the runs that were cut, in the order of the line, one
+// wavefront a row: a run of n + 1 pieces has n workgroups that begin inside
+// of it, and these share its rows. (A workgroup for every four rows of every
+// one of them, most of which had nothing to do, took 9 us; this takes 5.)
+constexpr int kJoinWaves = 16;
+
+template <int DIM, int NQ, bool BF16>
+__global__ __launch_bounds__(kJoinWaves * 64) void kv4_attention_join_kernel(const AttnParams a) {
+  constexpr int kRows = 16 * NQ;
   constexpr int kPer = 8, kLanes = DIM / kPer;  // lanes that hold a row; the others take other pieces
   constexpr int kGroups = 64 / kLanes;
-  const int lane = threadIdx.x & 63;
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int heads = a.kv_heads * a.group;
-  if (id >= static_cast<int64_t>(a.rows) * heads) return;
-  const int row = static_cast<int>(id / heads), head = static_cast<int>(id - static_cast<int64_t>(row) * heads);
-  const int share = a.sched[a.batch].x;
-  int b = 0, qs;
-  if (a.q_start) {
-    // the last sequence that starts at or before the row
-    for (int b0 = 0; b0 < a.batch; b0 += 64) {
-      const bool before = b0 + lane < a.batch && a.q_start[b0 + lane] <= row;
-      const unsigned long long m = __ballot(before);
-      if (m) b = b0 + 63 - __builtin_clzll(m);
-      if (m != ~0ull) break;
-    }
-    b = __builtin_amdgcn_readfirstlane(b);
-    qs = a.q_start[b];
-    if (row < qs || row - qs >= a.max_q || row >= a.q_start[b + 1]) return;  // a row of no sequence
-  } else {
-    b = row / a.max_q;
-    qs = b * a.max_q;
-  }
-  const int4 sc = a.sched[b];
-  const int r = (row - qs) * a.group + head % a.group;
-  const int first = sc.x + (r / unit_rows * a.kv_heads + head / a.group) * (sc.y + kRunCost) + kRunCost;
-  const int w0 = first / share, w1 = (first + sc.y - 1) / share;
-  if (w0 == w1) return;  // written by the workgroup that had all of it
-  const float2* ml = reinterpret_cast<const float2*>(a.part + static_cast<int64_t>(2 * a.groups) * unit_rows * DIM);
-  const auto piece = [&](int w) { return static_cast<int64_t>(2 * w + (w == w0)) * unit_rows + r % unit_rows; };
-  float mx = kNoToken;
-  for (int w = w0 + lane; w <= w1; w += 64) mx = fmaxf(mx, ml[piece(w)].x);
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
-  float l = 0.f, v[kPer] = {};
+  const int lane = threadIdx.x & 63, w = blockIdx.x;
+  const Cut c = a.cuts[w];
+  if (c.rows == 0) return;  // else first < w <= last
   const int gr = lane / kLanes, d = lane % kLanes * kPer;
-#pragma unroll 4
-  for (int w = w0 + gr; w <= w1; w += kGroups) {
-    const float2 x = ml[piece(w)];
-    const float* src = a.part + piece(w) * DIM + d;
-    const f4 v0 = *reinterpret_cast<const f4*>(src), v1 = *reinterpret_cast<const f4*>(src + 4);
-    const float p = __builtin_amdgcn_exp2f(x.x - mx);
-    l += p * x.y;
+  const float2* ml = reinterpret_cast<const float2*>(a.part + static_cast<int64_t>(2 * a.groups) * kRows * DIM);
+  const int n = c.last - c.first;
+  for (int r = w - c.first - 1 + __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6) * n; r < c.rows;
+       r += n * kJoinWaves) {
+    const auto piece = [&](int x) { return (2 * x + (x == c.first)) * kRows + r; };
+    float mx = kNoToken;
+#pragma unroll 1
+    for (int x = c.first + lane; x <= c.last; x += 64) mx = fmaxf(mx, ml[piece(x)].x);
+#pragma unroll 1
+    for (int o = 1; o < 64; o <<= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
+    float l = 0.f, v[kPer] = {};
+#pragma unroll 8
+    for (int x = c.first + gr; x <= c.last; x += kGroups) {
+      const float2 q = ml[piece(x)];
+      const float* src = a.part + static_cast<int64_t>(piece(x)) * DIM + d;
+      const f4 v0 = *reinterpret_cast<const f4*>(src), v1 = *reinterpret_cast<const f4*>(src + 4);
+      const float p = __builtin_amdgcn_exp2f(q.x - mx);
+      l += p * q.y;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[e] += p * v0[e];
-      v[4 + e] += p * v1[e];
+      for (int e = 0; e < 4; ++e) {
+        v[e] += p * v0[e];
+        v[4 + e] += p * v1[e];
+      }
+    }
+#pragma unroll 1
+    for (int o = kLanes; o < 64; o <<= 1) {
+      l += __shfl_xor(l, o);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) v[e] += __shfl_xor(v[e], o);
+    }
+    if (gr == 0) {
+      const float up = l > 0.f ? a.v_scale / l : (l == 0.f ? 0.f : l);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) v[e] *= up;
+      const int qi = (c.row0 + r) / a.group, hh = (c.row0 + r) - qi * a.group;
+      const int64_t to = static_cast<int64_t>(c.qs + qi) * (a.kv_heads * a.group) + c.head * a.group + hh;
+      store_out8<BF16>(a.out, to * DIM + d, v);
+      if (d == 0 && a.lse)
+        a.lse[to] = l == 0.f ? -__builtin_inff() : (__builtin_amdgcn_logf(l) + mx) * 0.69314718055994531f;
     }
   }
-#pragma unroll
-  for (int o = kLanes; o < 64; o <<= 1) {
-    l += __shfl_xor(l, o);
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) v[e] += __shfl_xor(v[e], o);
-  }
-  if (gr != 0) return;
-  const float up = l > 0.f ? a.v_scale / l : (l == 0.f ? 0.f : l);
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) v[e] *= up;
-  store_out8<BF16>(a.out, id * DIM + d, v);
-  if (d == 0 && a.lse)
-    a.lse[id] = l == 0.f ? -__builtin_inff() : (__builtin_amdgcn_logf(l) + mx) * 0.69314718055994531f;
 }
 
 template <int DIM, int NQ, bool BF16>
@@ -802,9 +815,8 @@ hipError_t launch_as(const AttnParams& a, hipStream_t stream) {
   kv4_attention_kernel<DIM, NQ, BF16><<<dim3(grid), dim3(kW * 64), 0, stream>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.groups == 0) return e;
-  const int64_t heads = static_cast<int64_t>(a.rows) * a.kv_heads * a.group;
-  kv4_attention_join_kernel<DIM, BF16>
-      <<<dim3(static_cast<uint32_t>((heads + 3) / 4)), dim3(256), 0, stream>>>(a, 16 * NQ);
+  kv4_attention_join_kernel<DIM, NQ, BF16>
+      <<<dim3(static_cast<uint32_t>(a.groups)), dim3(kJoinWaves * 64), 0, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -854,8 +866,8 @@ hipError_t launch_kv4_attention(const qpn_kv4_cache& c, const qpn_kv4_attention_
   a.row_tiles = p.row_tiles, a.groups = p.groups, a.min_share = p.min_share;
   a.f = x.scale * 1.44269504088896341f * c.k_scale;
   a.v_scale = c.v_scale;
-  a.sched = static_cast<int4*>(workspace);
-  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.sched_bytes);
+  a.cuts = static_cast<Cut*>(workspace);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.cut_bytes);
   return x.dtype == QPN_DT_BF16 ? launch_dim<true>(c.head_dim, p.tiles16, a, stream)
                                 : launch_dim<false>(c.head_dim, p.tiles16, a, stream);
 }

@@ -53,8 +53,8 @@ int main() {
                 CHECK(line + 2 * p.groups + p.min_share * static_cast<int64_t>(p.groups) <= INT32_MAX);
                 const size_t piece = static_cast<size_t>(16) * p.tiles16 * (dim + 2) * 4;
                 CHECK(p.partial_bytes == 2 * static_cast<size_t>(p.groups) * piece);
-                CHECK(p.sched_bytes >= (static_cast<size_t>(batch) + 1) * 16 && p.sched_bytes % 16 == 0);
-                CHECK(p.total_bytes == 0 || p.total_bytes == p.sched_bytes + p.partial_bytes);
+                CHECK(p.cut_bytes == static_cast<size_t>(p.groups) * 32);
+                CHECK(p.total_bytes == 0 || p.total_bytes == p.cut_bytes + p.partial_bytes);
                 CHECK((p.total_bytes == 0) == (p.groups == 0 || batch == 0 || a.rows == 0));
                 CHECK(qpn_kv4_attention_workspace_bytes(&c, &a) == p.total_bytes);
               }

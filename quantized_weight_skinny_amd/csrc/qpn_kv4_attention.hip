@@ -444,10 +444,11 @@ __global__ __launch_bounds__(kW * 64, attn_waves_per_simd(DIM, NQ)) void kv4_att
   };
   // They are asked for before the first keys and values and made into
   // fragments while those come; in LDS, wavefront n does tile n for all four.
-  // Two tiles of 256 would have too many registers on the way: those queries
-  // come first, eight elements at a time, bf16 rows twice.
+  // Two tiles (of 128 at three wavefronts a SIMD, of 256) would have too many
+  // registers on the way: those queries come first, eight elements at a time,
+  // bf16 rows twice.
   static_assert(NQ <= kW, "a wavefront prepares one tile");
-  constexpr bool kQueriesFirst = NQ * DIM == 512;
+  constexpr bool kQueriesFirst = NQ == 2 && DIM >= 128;
   u4 raw[kQueriesFirst ? 1 : kQueriesInLds ? 1 : NQ][kQueriesFirst ? 1 : kSteps];
   if constexpr (kQueriesFirst) {
     if (wave < NQ) {
@@ -596,19 +597,35 @@ __global__ __launch_bounds__(kW * 64, attn_waves_per_simd(DIM, NQ)) void kv4_att
   // behind goes first.
   const int quarter = (mine + 3) / 4;
   __builtin_amdgcn_s_setprio(3);
-  for (int j = 0; j < mine; ++j) {
+  // (Where the registers hold two tiles, three row tiles of 128, the whole next
+  // tile is asked for before this one's scores: 57 -> 54 us over 131072 tokens.)
+  constexpr bool kTwo = NQ * DIM == 384;
+  auto step = [&](Tile<DIM>& t, Tile<DIM>& u, int j) {
     if (j == quarter) __builtin_amdgcn_s_setprio(2);
     if (j == 2 * quarter) __builtin_amdgcn_s_setprio(1);
     if (j == 3 * quarter) __builtin_amdgcn_s_setprio(0);
     const int tok = (t0 + wave + j * kW) * kTileTokens;
+    Place r;
+    bool none0, none1;  // before place(j + 1) looks up the next 64
+    if constexpr (kTwo) {
+      none0 = absent[0] >> (j & 63) & 1, none1 = absent[1] >> (j & 63) & 1;
+      r = place(j + 1);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) load_keys<DIM>(u, h, r.seg[h], lane_at, r.codes[h], r.scales[h]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) load_vals<DIM>(u, h, r.seg[h], lane_at, r.codes[h], r.scales[h]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     f4 sc[2][NQ];
     scores<DIM, NQ>(t, query, sc);
-    const bool none0 = absent[0] >> (j & 63) & 1, none1 = absent[1] >> (j & 63) & 1;
-    __builtin_amdgcn_sched_barrier(0);
-    const Place r = place(j + 1);
+    if constexpr (!kTwo) {
+      none0 = absent[0] >> (j & 63) & 1, none1 = absent[1] >> (j & 63) & 1;
+      __builtin_amdgcn_sched_barrier(0);
+      r = place(j + 1);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) load_keys<DIM>(t, h, r.seg[h], lane_at, r.codes[h], r.scales[h]);
-    __builtin_amdgcn_sched_barrier(0);
+      for (int h = 0; h < 2; ++h) load_keys<DIM>(t, h, r.seg[h], lane_at, r.codes[h], r.scales[h]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     uint32_t vs[2] = {t.vs[0], t.vs[1]};
     const bool whole =
         tok + kTileTokens - 1 <= first_pos && (win == 0 || tok > last_pos - win) && !none0 && !none1;
@@ -673,9 +690,21 @@ __global__ __launch_bounds__(kW * 64, attn_waves_per_simd(DIM, NQ)) void kv4_att
     }
     values<DIM, NQ>(t, vs, p, o);
     __builtin_amdgcn_sched_barrier(0);
+    if constexpr (!kTwo) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) load_vals<DIM>(t, h, r.seg[h], lane_at, r.codes[h], r.scales[h]);
-    __builtin_amdgcn_sched_barrier(0);
+      for (int h = 0; h < 2; ++h) load_vals<DIM>(t, h, r.seg[h], lane_at, r.codes[h], r.scales[h]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  if constexpr (kTwo) {
+    Tile<DIM> u;
+    for (int j = 0; j < mine; j += 2) {
+      step(t, u, j);
+      if (j + 1 >= mine) break;
+      step(u, t, j + 1);
+    }
+  } else {
+    for (int j = 0; j < mine; ++j) step(t, t, j);
   }
 
   const AttnParams& z = reread(params);

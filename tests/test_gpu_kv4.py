@@ -293,6 +293,17 @@ def test_attention_many_sequences():
     c.check(c.run())
 
 
+def test_attention_many_sequences_cut_into_shares():
+    """The same where the tiles are laid end to end: more sequences than lanes,
+    some empty, some without rows, one much longer than the others."""
+    rng = np.random.default_rng(2)
+    kv = [int(x) for x in rng.integers(0, 90, 140)]
+    rows = [int(x) for x in rng.integers(0, 4, 140)]
+    kv[77], rows[77], kv[139], rows[139] = 5000, 3, 2300, 2
+    c = Case(24, kv, rows, 3, 1, 64, 32, "bf16")
+    c.check(c.run())
+
+
 def test_attention_long_block():
     """A block of many rows: several row tiles a sequence, causal across tiles."""
     c = Case(12, [150, 70], [130, 70], 3, 1, 128, 32, "fp16")

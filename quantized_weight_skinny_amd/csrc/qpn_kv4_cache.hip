@@ -77,19 +77,66 @@ __device__ __forceinline__ uint2 load_block(const BlockRef& r) {
   }
 }
 
-// One block of 16 values: its scale byte and its codes (two dwords).
-__device__ __forceinline__ uint32_t quantize_block(const float (&v)[16], float s_t, uint32_t& lo, uint32_t& hi) {
-  float amax = 0.f;
+// One block of 16 values (as 16-bit words): its scale byte and its codes (two
+// dwords). `plain`: the tensor scale is far enough from the ends of fp32 for
+// the quotients below.
+//
+// The codes are those of fp32 division and the nearest-even rule. A division
+// an element would be a third of the kernel's instructions, so the block
+// divides once: with r = 1 / d correctly rounded and q = x * r, off by at most
+// an ulp, q + (x - q d) r, the residual exact in a fused multiply-add, is the
+// correctly rounded x / d. Blocks with an infinity or NaN take the division.
+// 16389 tokens of 2 x 1024 elements: 37 us with divisions and a comparison
+// for every midpoint, 21 us so (4.1 TB/s of values in and codes out).
+template <bool BF16>
+__device__ __forceinline__ uint32_t quantize_block(const u4 (&w)[2], float s_t, bool plain, uint32_t& lo, uint32_t& hi) {
+  // magnitudes of 16-bit floats are ordered as their bits are
+  typedef unsigned short us2 __attribute__((ext_vector_type(2)));
+  us2 top2 = {0, 0};
 #pragma unroll
-  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(v[i]));  // a NaN is passed over
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t x = w[j / 4][j % 4] & 0x7FFF7FFFu;
+    top2 = __builtin_elementwise_max(top2, __builtin_bit_cast(us2, x));
+  }
+  const uint32_t top = max(static_cast<uint32_t>(top2[0]), static_cast<uint32_t>(top2[1]));
+  constexpr uint32_t kInf = BF16 ? 0x7F80u : 0x7C00u;
+  float v[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) v[e] = widen16<BF16>((w[e / 8][e / 2 % 4] >> (16 * (e & 1))) & 0xFFFFu);
+  float amax = widen16<BF16>(top);
+  if (top > kInf) {
+    // the largest that is a number
+    amax = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(v[e]));
+  }
   const uint32_t sc = encode_e4m3(amax / 6.0f / s_t);
   const float d = decode_e4m3(sc) * s_t;
   lo = 0u, hi = 0u;
+  if (plain && top < kInf && d != 0.f) {
+    const float r = 1.0f / d;
+    float q[16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t c = d == 0.f ? ((__float_as_uint(v[i]) >> 28) & 0x8u) : encode_e2m1(v[i] / d);
-    if (i < 8) lo |= c << (4 * i);
-    else hi |= c << (4 * (i - 8));
+    for (int e = 0; e < 16; ++e) {
+      const float q0 = v[e] * r;
+      // (a zero keeps its sign)
+      q[e] = copysignf(fmaf(fmaf(-q0, d, v[e]), r, q0), v[e]);
+    }
+    lo = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(lo, q[0], q[1], 1.0f, 0);
+    lo = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(lo, q[2], q[3], 1.0f, 1);
+    lo = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(lo, q[4], q[5], 1.0f, 2);
+    lo = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(lo, q[6], q[7], 1.0f, 3);
+    hi = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(hi, q[8], q[9], 1.0f, 0);
+    hi = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(hi, q[10], q[11], 1.0f, 1);
+    hi = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(hi, q[12], q[13], 1.0f, 2);
+    hi = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(hi, q[14], q[15], 1.0f, 3);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const uint32_t c = d == 0.f ? ((__float_as_uint(v[e]) >> 28) & 0x8u) : encode_e2m1(v[e] / d);
+      if (e < 8) lo |= c << (4 * e);
+      else hi |= c << (4 * (e - 8));
+    }
   }
   return sc;
 }
@@ -99,26 +146,23 @@ struct Source {
   int64_t ts, hs;
   int32_t aligned;  // rows start on 16 bytes
   float scale;
+  bool plain;       // the scale lies between 2^-60 and 2^60
 };
 
 template <int DIM, bool BF16, bool V>
 __device__ __forceinline__ void append_block(const PoolRef& p, const Source& s, int64_t t, int64_t slot, int head,
                                              int blk) {
   const uint16_t* src = s.data + t * s.ts + head * s.hs + blk * 16;
-  float v[16];
+  u4 w[2];
   if (s.aligned) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const u4 w = reinterpret_cast<const u4*>(src)[j];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[8 * j + e] = widen16<BF16>((w[e / 2] >> (16 * (e & 1))) & 0xFFFFu);
-    }
+    for (int j = 0; j < 2; ++j) w[j] = reinterpret_cast<const u4*>(src)[j];
   } else {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = widen16<BF16>(src[e]);
+    for (int j = 0; j < 8; ++j) w[j / 4][j % 4] = src[2 * j] | static_cast<uint32_t>(src[2 * j + 1]) << 16;
   }
   uint32_t lo, hi;
-  const uint32_t sc = quantize_block(v, s.scale, lo, hi);
+  const uint32_t sc = quantize_block<BF16>(w, s.scale, s.plain, lo, hi);
   store_block<DIM, V>(block_ref<DIM, V>(p, slot, head, blk), lo, hi, sc);
 }
 
@@ -255,7 +299,7 @@ hipError_t launch_kv4_append(const qpn_kv4_cache& c, int32_t layer, const void* 
   const PoolRef p = pool_ref(c, layer);
   const auto source = [](const void* x, int64_t ts, int64_t hs, float scale) {
     const bool al = reinterpret_cast<uintptr_t>(x) % 16 == 0 && ts % 8 == 0 && hs % 8 == 0;
-    return Source{static_cast<const uint16_t*>(x), ts, hs, al, scale};
+    return Source{static_cast<const uint16_t*>(x), ts, hs, al, scale, scale > 0x1p-60f && scale < 0x1p60f};
   };
   const int64_t most = tokens_per_launch(c.kv_heads, c.head_dim);
   for (int64_t t = 0; t < tokens; t += most) {

@@ -25,6 +25,19 @@
 // largest) and p. p is kept between 2^8 (at the reference) and 2^15: a row's
 // reference moves only when a score passes it by 2^7, which a wavefront sees
 // with one vote, and p as small as 2^-22 of the largest is a normal fp16.
+//
+// What bounds it. For 32 tokens of 128 elements the codes take 64 conversions
+// and 64 multiplications (the conversion's own scale is a power of two, the
+// blocks' are not) and 16 instructions to pair V's; every row tile adds 8
+// exponentials at two slots each, 24 adds and multiply-adds, 4 conversions, 6
+// for the maximum and 16 MFMAs. At three row tiles (8 rows of 5 heads) that
+// counts to 1600 cycles a SIMD; 1670 are measured, with two wavefronts, which
+// a SIMD needs: one alone issues a vector instruction every 8 cycles, two or
+// more every 4 to 5. So 131072 tokens of 8 heads (151 MB) take 27 us of vector
+// instructions against 25 us of memory, and the call 50: the rest is the
+// launch (2), the shares' counting and first loads (6), joining wavefronts (3)
+// and pieces (6), and what memory's latency leaves open. At one row tile (one
+// row, four wavefronts a SIMD) 24 sequences' 180 MB take 39 us.
 #include "qpn_device.hpp"
 #include "qpn_decode_internal.hpp"
 
@@ -35,7 +48,8 @@ constexpr int kW = kAttnWaves;
 constexpr float kNoToken = -1e30f;  // a row's reference before it has seen a token
 constexpr float kBias = 8.0f, kHeadroom = 15.0f;
 // What a run costs besides its tiles, in tiles: its queries, the first loads'
-// latency and the joining of the wavefronts.
+// latency and the joining of the wavefronts (4 to 6 us where a tile takes 0.2
+// to 0.4). 48 ragged sequences 127 us with 0, 87 with 12, 81 with 20.
 constexpr int kRunCost = 20;
 
 struct AttnParams {
@@ -320,7 +334,7 @@ __global__ __launch_bounds__(kW * 64, attn_waves_per_simd(DIM, NQ)) void kv4_att
     seq = sequence(a0, b, kRows);
     at = (group_id - b * per) * (seq.tiles + kRunCost);
     end = at + seq.tiles + kRunCost;
-    if (at >= seq.rt * a0.kv_heads * (seq.tiles + kRunCost)) return;  // the sequence has fewer row tiles than the longest
+    if (at >= seq.rt * a0.kv_heads * (seq.tiles + kRunCost)) return;  // fewer row tiles than the longest has
   } else {
     int total = 0;
     // of the last 64 sequences: a lane's, its part of the line, and the running sum
@@ -366,417 +380,419 @@ __global__ __launch_bounds__(kW * 64, attn_waves_per_simd(DIM, NQ)) void kv4_att
   }
   bool first_run = true;
   while (true) {
-  // (what follows from the lane is worked out again for every run: kept from
-  // one to the next it would take registers that the occupancy needs;
-  // and so are the arguments, which come from the scalar cache)
-  asm volatile("" : "+v"(tid), "+v"(lane));
-  const AttnParams& a = reread(params);
-  const int i = lane & 15, g = lane >> 4;
-  const Seq s = seq;
-  const int cost = s.tiles + kRunCost;
-  const int run = (at - base) / cost, from = at - base - run * cost, to = min(cost, from + end - at);
-  const int tile0 = max(0, from - kRunCost), tiles = max(0, to - kRunCost) - tile0;
-  at += to - from;
-  const int rtile = run / a.kv_heads, head = run - rtile * a.kv_heads;
-  const bool alone = tiles == s.tiles;  // the whole run
-  // The rows: row r of the row tile is query row r / group, head r % group.
-  const int row0 = rtile * kRows, nrows = min(s.ql * a.group - row0, kRows);
-  if (first_run && a.groups && tid == 0) {
-    // where this run's first tile and its last lie on the line
-    const int begin = base + run * cost + kRunCost;
-    a.cuts[group_id] = Cut{tile0 > 0 ? nrows : 0, begin / share, (begin + s.tiles - 1) / share, s.qs, row0, head, {0, 0}};
-  }
-  first_run = false;
-  if (tiles > 0) {
-
-  h8 qreg[kQueriesInLds ? 1 : NQ][kSteps];
-  float f[NQ], m[NQ], l[NQ];
-  f4 o[NQ][kBlocks];
-  // Row tile n's queries as a wavefront's lanes hold them: a lane's part of its
-  // row in memory, eight elements of it as they lie there, and as a fragment.
-  const auto row_of = [&](int n) {
-    const int r = n * 16 + i;
-    const int qi = (row0 + r) / a.group, hh = (row0 + r) - qi * a.group;
-    const bool live = r < nrows;  // (a row past the last loads the first)
-    const int64_t row_at = static_cast<int64_t>(s.qs + (live ? qi : 0)) * a.q_ts +
-                           static_cast<int64_t>(head * a.group + (live ? hh : 0)) * a.q_hs + g * (DIM / 4);
-    return static_cast<const uint16_t*>(a.q) + row_at;
-  };
-  const auto eight = [&](const uint16_t* src, int c) {
-    u4 x;
-    if (a.q_aligned) {
-      x = *reinterpret_cast<const u4*>(src + c * 8);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = src[c * 8 + 2 * e] | static_cast<uint32_t>(src[c * 8 + 2 * e + 1]) << 16;
+    // (what follows from the lane is worked out again for every run: kept from
+    // one to the next it would take registers that the occupancy needs;
+    // and so are the arguments, which come from the scalar cache)
+    asm volatile("" : "+v"(tid), "+v"(lane));
+    const AttnParams& a = reread(params);
+    const int i = lane & 15, g = lane >> 4;
+    const Seq s = seq;
+    const int cost = s.tiles + kRunCost;
+    const int run = (at - base) / cost, from = at - base - run * cost, to = min(cost, from + end - at);
+    const int tile0 = max(0, from - kRunCost), tiles = max(0, to - kRunCost) - tile0;
+    at += to - from;
+    const int rtile = run / a.kv_heads, head = run - rtile * a.kv_heads;
+    const bool alone = tiles == s.tiles;  // the whole run
+    // The rows: row r of the row tile is query row r / group, head r % group.
+    const int row0 = rtile * kRows, nrows = min(s.ql * a.group - row0, kRows);
+    if (first_run && a.groups && tid == 0) {
+      // where this run's first tile and its last lie on the line
+      const int begin = base + run * cost + kRunCost;
+      a.cuts[group_id] = Cut{tile0 > 0 ? nrows : 0, begin / share, (begin + s.tiles - 1) / share, s.qs, row0, head,
+                             {0, 0}};
     }
-    return x;
-  };
-  // bf16: the exponent (clamped: a row below 2^-60 by 2^60; inf and NaN stay
-  // themselves) that brings a row's largest magnitude to [1, 2).
-  const auto larger = [](uint32_t top, const u4& x) {
+    first_run = false;
+    if (tiles > 0) {
+      h8 qreg[kQueriesInLds ? 1 : NQ][kSteps];
+      float f[NQ], m[NQ], l[NQ];
+      f4 o[NQ][kBlocks];
+      // Row tile n's queries as a wavefront's lanes hold them: a lane's part of its
+      // row in memory, eight elements of it as they lie there, and as a fragment.
+      const auto row_of = [&](int n) {
+        const int r = n * 16 + i;
+        const int qi = (row0 + r) / a.group, hh = (row0 + r) - qi * a.group;
+        const bool live = r < nrows;  // (a row past the last loads the first)
+        const int64_t row_at = static_cast<int64_t>(s.qs + (live ? qi : 0)) * a.q_ts +
+                               static_cast<int64_t>(head * a.group + (live ? hh : 0)) * a.q_hs + g * (DIM / 4);
+        return static_cast<const uint16_t*>(a.q) + row_at;
+      };
+      const auto eight = [&](const uint16_t* src, int c) {
+        u4 x;
+        if (a.q_aligned) {
+          x = *reinterpret_cast<const u4*>(src + c * 8);
+        } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) top = max(max(top, x[e] & 0x7FFFu), (x[e] >> 16) & 0x7FFFu);
-    return top;
-  };
-  const auto exponent = [](uint32_t top) {
-    top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16)));
-    top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32)));
-    return min(max(static_cast<int>(top >> 7), 67), 252) - 127;
-  };
-  const auto fragment = [&](int n, u4 x, int e2) {
-    if (n * 16 + i >= nrows) x = u4{0u, 0u, 0u, 0u};
-    if constexpr (BF16) {
-      const float down = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
-      h8 q;
+          for (int e = 0; e < 4; ++e) x[e] = src[c * 8 + 2 * e] | static_cast<uint32_t>(src[c * 8 + 2 * e + 1]) << 16;
+        }
+        return x;
+      };
+      // bf16: the exponent (clamped: a row below 2^-60 by 2^60; inf and NaN stay
+      // themselves) that brings a row's largest magnitude to [1, 2).
+      const auto larger = [](uint32_t top, const u4& x) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        q[2 * e] = static_cast<_Float16>(__uint_as_float(x[e] << 16) * down);
-        q[2 * e + 1] = static_cast<_Float16>(__uint_as_float(x[e] & 0xFFFF0000u) * down);
-      }
-      return q;
-    } else {
-      return __builtin_bit_cast(h8, x);
-    }
-  };
-  const auto factor = [&](int e2) {
-    return BF16 ? a.f * __uint_as_float(static_cast<uint32_t>(127 + e2) << 23) : a.f;
-  };
-  // They are asked for before the first keys and values and made into
-  // fragments while those come; in LDS, wavefront n does tile n for all four.
-  // Two tiles (of 128 at three wavefronts a SIMD, of 256) would have too many
-  // registers on the way: those queries come first, eight elements at a time,
-  // bf16 rows twice.
-  static_assert(NQ <= kW, "a wavefront prepares one tile");
-  constexpr bool kQueriesFirst = NQ == 2 && DIM >= 128;
-  u4 raw[kQueriesFirst ? 1 : kQueriesInLds ? 1 : NQ][kQueriesFirst ? 1 : kSteps];
-  if constexpr (kQueriesFirst) {
-    if (wave < NQ) {
-      const uint16_t* src = row_of(wave);
-      int e2 = 0;
-      if constexpr (BF16) {
-        uint32_t top = 0;
-#pragma unroll 1
-        for (int c = 0; c < kSteps; ++c) top = larger(top, eight(src, c));
-        e2 = exponent(top);
-      }
-#pragma unroll 1
-      for (int c = 0; c < kSteps; ++c)
-        sh.q[(wave * kSteps + c) * 64 + lane] = __builtin_bit_cast(u4, fragment(wave, eight(src, c), e2));
-      if (g == 0) fs[wave * 16 + i] = factor(e2);
-    }
-  } else if constexpr (kQueriesInLds) {
-    if (wave < NQ) {
-      const uint16_t* src = row_of(wave);
-#pragma unroll
-      for (int c = 0; c < kSteps; ++c) raw[0][c] = eight(src, c);
-    }
-  } else {
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      const uint16_t* src = row_of(n);
-#pragma unroll
-      for (int c = 0; c < kSteps; ++c) raw[n][c] = eight(src, c);
-    }
-  }
-
-  // The tiles in hand, cut to what this row tile's rows see at all.
-  const int first_pos = s.len - s.ql + row0 / a.group, last_pos = s.len - s.ql + (row0 + nrows - 1) / a.group;
-  const int win = a.window;
-  int t0 = s.lo + tile0, t1 = t0 + tiles;
-  t1 = min(t1, last_pos / kTileTokens + (last_pos >= 0));
-  if (win) t0 = max(t0, max(0, first_pos - win + 1) / kTileTokens);
-  const int mine = t1 > t0 + wave && a.pages > 0 ? (t1 - t0 - wave + kW - 1) / kW : 0;  // this wavefront's tiles
-  const int page = 1 << a.page_shift;
-  const int32_t* table = a.table + static_cast<int64_t>(b) * a.table_stride;
-  const uint8_t* head_base = a.cache + static_cast<int64_t>(head) * a.seg_bytes;
-
-  // The page segments of the wavefront's next 64 tiles, a lane each, and which
-  // of their halves have none. A half's loads take their base from here and
-  // their place in the page from the token, in scalar registers throughout.
-  uint64_t base_of[2], absent[2] = {0, 0};
-  auto pages_from = [&](int j0) {
-    const int j = j0 + lane;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int tok = (t0 + wave + j * kW) * kTileTokens + 16 * h;
-      int p = -1;
-      if (j < mine && tok < s.len) p = table[tok >> a.page_shift];
-      const bool none = p < 0 || p >= a.pages;
-      base_of[h] = reinterpret_cast<uint64_t>(head_base) + static_cast<uint64_t>(none ? 0 : p) * a.page_bytes;
-      absent[h] = __ballot(none);
-    }
-  };
-  // Tile j's place: the segments of its halves and their tokens' offsets in
-  // the codes and in the scales. Past the last tile the segments are empty:
-  // loads there bring zeros and no traffic, and as every step has the same
-  // loads, a wait for the older ones need not be a wait for all.
-  struct Place {
-    __amdgpu_buffer_rsrc_t seg[2];
-    int codes[2], scales[2];
-  };
-  const auto place = [&](int j) {
-    Place r;
-    if ((j & 63) == 0) pages_from(j);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(base_of[h]), j & 63);
-      const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(base_of[h] >> 32), j & 63);
-      r.seg[h] = segment_of(reinterpret_cast<const uint8_t*>(static_cast<uint64_t>(hi) << 32 | lo),
-                            j < mine ? a.seg_bytes : 0);
-      const int off = ((t0 + wave + j * kW) * kTileTokens + 16 * h) & (page - 1);
-      r.codes[h] = off * (DIM / 2);
-      r.scales[h] = off * (DIM / 16);
-    }
-    return r;
-  };
-  Tile<DIM> t;
-  const LaneOffsets<DIM> lane_at(lane, page);
-  if (mine > 0) {
-    const Place r = place(0);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) load_keys<DIM>(t, h, r.seg[h], lane_at, r.codes[h], r.scales[h]);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) load_vals<DIM>(t, h, r.seg[h], lane_at, r.codes[h], r.scales[h]);
-    __builtin_amdgcn_sched_barrier(0);
-  }
-  __builtin_amdgcn_sched_barrier(0);
-  const auto exponent_of = [&](const u4 (&x)[kQueriesFirst ? 1 : kSteps]) {
-    uint32_t top = 0;
-    if constexpr (BF16) {
-#pragma unroll
-      for (const u4& w : x) top = larger(top, w);
-      return exponent(top);
-    }
-    return 0;
-  };
-  if constexpr (kQueriesInLds) {
-    if constexpr (!kQueriesFirst) {
-      if (wave < NQ) {
-        const int e2 = exponent_of(raw[0]);
-#pragma unroll
-        for (int c = 0; c < kSteps; ++c)
-          sh.q[(wave * kSteps + c) * 64 + lane] = __builtin_bit_cast(u4, fragment(wave, raw[0][c], e2));
-        if (g == 0) fs[wave * 16 + i] = factor(e2);
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) f[n] = fs[n * 16 + i];
-  } else {
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      const int e2 = exponent_of(raw[n]);
-#pragma unroll
-      for (int c = 0; c < kSteps; ++c) qreg[n][c] = fragment(n, raw[n][c], e2);
-      f[n] = factor(e2);
-    }
-  }
-  const auto query = [&](int n, int c) -> h8 {
-    if constexpr (kQueriesInLds)
-      return __builtin_bit_cast(h8, sh.q[(n * kSteps + c) * 64 + lane]);
-    else
-      return qreg[n][c];
-  };
-#pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    m[n] = kNoToken;
-    l[n] = 0.f;
-#pragma unroll
-    for (int j = 0; j < kBlocks; ++j) o[n][j] = f4{0.f, 0.f, 0.f, 0.f};
-  }
-
-  // The keys of the next tile are on their way during this one's softmax and
-  // values, its values during the next one's scores: one set of registers
-  // each, and the other wavefronts of the SIMD to fill what is left.
-  //
-  // A SIMD serves the older of its wavefronts first, and the workgroup that
-  // came second to a compute unit would end a third later than the first. So
-  // a wavefront's priority falls with every quarter of its tiles: whoever is
-  // behind goes first.
-  const int quarter = (mine + 3) / 4;
-  __builtin_amdgcn_s_setprio(3);
-  // (Where the registers hold two tiles, three row tiles of 128, the whole next
-  // tile is asked for before this one's scores: 57 -> 54 us over 131072 tokens.)
-  constexpr bool kTwo = NQ * DIM == 384;
-  auto step = [&](Tile<DIM>& t, Tile<DIM>& u, int j) {
-    if (j == quarter) __builtin_amdgcn_s_setprio(2);
-    if (j == 2 * quarter) __builtin_amdgcn_s_setprio(1);
-    if (j == 3 * quarter) __builtin_amdgcn_s_setprio(0);
-    const int tok = (t0 + wave + j * kW) * kTileTokens;
-    Place r;
-    bool none0, none1;  // before place(j + 1) looks up the next 64
-    if constexpr (kTwo) {
-      none0 = absent[0] >> (j & 63) & 1, none1 = absent[1] >> (j & 63) & 1;
-      r = place(j + 1);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) load_keys<DIM>(u, h, r.seg[h], lane_at, r.codes[h], r.scales[h]);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) load_vals<DIM>(u, h, r.seg[h], lane_at, r.codes[h], r.scales[h]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    f4 sc[2][NQ];
-    scores<DIM, NQ>(t, query, sc);
-    if constexpr (!kTwo) {
-      none0 = absent[0] >> (j & 63) & 1, none1 = absent[1] >> (j & 63) & 1;
-      __builtin_amdgcn_sched_barrier(0);
-      r = place(j + 1);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) load_keys<DIM>(t, h, r.seg[h], lane_at, r.codes[h], r.scales[h]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    uint32_t vs[2] = {t.vs[0], t.vs[1]};
-    const bool whole =
-        tok + kTileTokens - 1 <= first_pos && (win == 0 || tok > last_pos - win) && !none0 && !none1;
-    if (!whole) {
-      // Scores of unseen tokens become -inf whatever the cache holds there,
-      // and the values of tokens past the end or of absent pages are zeroed:
-      // such bytes may decode to NaN, which a p of 0 would not remove. Bit b
-      // of a mask stands for token tok + 4 g + b.
-      const int mine0 = tok + 4 * g;
-      const auto up_to = [](int x) -> uint32_t { return x < 0 ? 0u : x >= 31 ? ~0u : (2u << x) - 1u; };
-      const uint32_t held = up_to(s.len - 1 - mine0) & ((none0 ? 0u : 0xFFFFu) | (none1 ? 0u : 0xFFFF0000u));
-      const auto bit = [](uint32_t w, int b) { return static_cast<uint32_t>(static_cast<int32_t>(w << (31 - b)) >> 31); };
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) vs[h] &= ~(0xFFu << (8 * e)) | bit(held, 16 * h + e);
-#pragma unroll
-      for (int n = 0; n < NQ; ++n) {
-        // (the row's position is worked out here, for the few tiles that need it)
-        const int pos = s.len - s.ql + (row0 + n * 16 + i) / a.group;
-        const uint32_t seen = held & up_to(pos - mine0) & (win ? ~up_to(pos - win - mine0) : ~0u);
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int e = 0; e < 4; ++e) top = max(max(top, x[e] & 0x7FFFu), (x[e] >> 16) & 0x7FFFu);
+        return top;
+      };
+      const auto exponent = [](uint32_t top) {
+        top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16)));
+        top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32)));
+        return min(max(static_cast<int>(top >> 7), 67), 252) - 127;
+      };
+      const auto fragment = [&](int n, u4 x, int e2) {
+        if (n * 16 + i >= nrows) x = u4{0u, 0u, 0u, 0u};
+        if constexpr (BF16) {
+          const float down = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
+          h8 q;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint32_t k = bit(seen, 16 * h + e);
-            sc[h][n][e] = __uint_as_float((__float_as_uint(sc[h][n][e]) & k) | (0xFF800000u & ~k));
+            q[2 * e] = static_cast<_Float16>(__uint_as_float(x[e] << 16) * down);
+            q[2 * e + 1] = static_cast<_Float16>(__uint_as_float(x[e] & 0xFFFF0000u) * down);
           }
-      }
-    }
-    float far = -__builtin_inff();
-    float top[NQ];
+          return q;
+        } else {
+          return __builtin_bit_cast(h8, x);
+        }
+      };
+      const auto factor = [&](int e2) {
+        return BF16 ? a.f * __uint_as_float(static_cast<uint32_t>(127 + e2) << 23) : a.f;
+      };
+      // They are asked for before the first keys and values and made into
+      // fragments while those come; in LDS, wavefront n does tile n for all four.
+      // Two tiles (of 128 at three wavefronts a SIMD, of 256) would have too many
+      // registers on the way: those queries come first, eight elements at a time,
+      // bf16 rows twice.
+      static_assert(NQ <= kW, "a wavefront prepares one tile");
+      constexpr bool kQueriesFirst = NQ == 2 && DIM >= 128;
+      u4 raw[kQueriesFirst ? 1 : kQueriesInLds ? 1 : NQ][kQueriesFirst ? 1 : kSteps];
+      if constexpr (kQueriesFirst) {
+        if (wave < NQ) {
+          const uint16_t* src = row_of(wave);
+          int e2 = 0;
+          if constexpr (BF16) {
+            uint32_t top = 0;
+#pragma unroll 1
+            for (int c = 0; c < kSteps; ++c) top = larger(top, eight(src, c));
+            e2 = exponent(top);
+          }
+#pragma unroll 1
+          for (int c = 0; c < kSteps; ++c)
+            sh.q[(wave * kSteps + c) * 64 + lane] = __builtin_bit_cast(u4, fragment(wave, eight(src, c), e2));
+          if (g == 0) fs[wave * 16 + i] = factor(e2);
+        }
+      } else if constexpr (kQueriesInLds) {
+        if (wave < NQ) {
+          const uint16_t* src = row_of(wave);
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      top[n] = max3(max3(sc[0][n][0], sc[0][n][1], sc[0][n][2]), sc[0][n][3], sc[1][n][0]);
-      top[n] = max2(max3(top[n], sc[1][n][1], sc[1][n][2]), sc[1][n][3]);
-      far = max2(far, fmaf(top[n], f[n], -m[n]));
-    }
-    if (__any(far > kHeadroom)) {
+          for (int c = 0; c < kSteps; ++c) raw[0][c] = eight(src, c);
+        }
+      } else {
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          const uint16_t* src = row_of(n);
+#pragma unroll
+          for (int c = 0; c < kSteps; ++c) raw[n][c] = eight(src, c);
+        }
+      }
+
+      // The tiles in hand, cut to what this row tile's rows see at all.
+      const int first_pos = s.len - s.ql + row0 / a.group, last_pos = s.len - s.ql + (row0 + nrows - 1) / a.group;
+      const int win = a.window;
+      int t0 = s.lo + tile0, t1 = t0 + tiles;
+      t1 = min(t1, last_pos / kTileTokens + (last_pos >= 0));
+      if (win) t0 = max(t0, max(0, first_pos - win + 1) / kTileTokens);
+      const int mine = t1 > t0 + wave && a.pages > 0 ? (t1 - t0 - wave + kW - 1) / kW : 0;  // this wavefront's tiles
+      const int page = 1 << a.page_shift;
+      const int32_t* table = a.table + static_cast<int64_t>(b) * a.table_stride;
+      const uint8_t* head_base = a.cache + static_cast<int64_t>(head) * a.seg_bytes;
+
+      // The page segments of the wavefront's next 64 tiles, a lane each, and which
+      // of their halves have none. A half's loads take their base from here and
+      // their place in the page from the token, in scalar registers throughout.
+      uint64_t base_of[2], absent[2] = {0, 0};
+      auto pages_from = [&](int j0) {
+        const int j = j0 + lane;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int tok = (t0 + wave + j * kW) * kTileTokens + 16 * h;
+          int p = -1;
+          if (j < mine && tok < s.len) p = table[tok >> a.page_shift];
+          const bool none = p < 0 || p >= a.pages;
+          base_of[h] = reinterpret_cast<uint64_t>(head_base) + static_cast<uint64_t>(none ? 0 : p) * a.page_bytes;
+          absent[h] = __ballot(none);
+        }
+      };
+      // Tile j's place: the segments of its halves and their tokens' offsets in
+      // the codes and in the scales. Past the last tile the segments are empty:
+      // loads there bring zeros and no traffic, and as every step has the same
+      // loads, a wait for the older ones need not be a wait for all.
+      struct Place {
+        __amdgpu_buffer_rsrc_t seg[2];
+        int codes[2], scales[2];
+      };
+      const auto place = [&](int j) {
+        Place r;
+        if ((j & 63) == 0) pages_from(j);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(base_of[h]), j & 63);
+          const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(base_of[h] >> 32), j & 63);
+          r.seg[h] = segment_of(reinterpret_cast<const uint8_t*>(static_cast<uint64_t>(hi) << 32 | lo),
+                                j < mine ? a.seg_bytes : 0);
+          const int off = ((t0 + wave + j * kW) * kTileTokens + 16 * h) & (page - 1);
+          r.codes[h] = off * (DIM / 2);
+          r.scales[h] = off * (DIM / 16);
+        }
+        return r;
+      };
+      Tile<DIM> t;
+      const LaneOffsets<DIM> lane_at(lane, page);
+      if (mine > 0) {
+        const Place r = place(0);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) load_keys<DIM>(t, h, r.seg[h], lane_at, r.codes[h], r.scales[h]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) load_vals<DIM>(t, h, r.seg[h], lane_at, r.codes[h], r.scales[h]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      const auto exponent_of = [&](const u4 (&x)[kQueriesFirst ? 1 : kSteps]) {
+        uint32_t top = 0;
+        if constexpr (BF16) {
+#pragma unroll
+          for (const u4& w : x) top = larger(top, w);
+          return exponent(top);
+        }
+        return 0;
+      };
+      if constexpr (kQueriesInLds) {
+        if constexpr (!kQueriesFirst) {
+          if (wave < NQ) {
+            const int e2 = exponent_of(raw[0]);
+#pragma unroll
+            for (int c = 0; c < kSteps; ++c)
+              sh.q[(wave * kSteps + c) * 64 + lane] = __builtin_bit_cast(u4, fragment(wave, raw[0][c], e2));
+            if (g == 0) fs[wave * 16 + i] = factor(e2);
+          }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) f[n] = fs[n * 16 + i];
+      } else {
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          const int e2 = exponent_of(raw[n]);
+#pragma unroll
+          for (int c = 0; c < kSteps; ++c) qreg[n][c] = fragment(n, raw[n][c], e2);
+          f[n] = factor(e2);
+        }
+      }
+      const auto query = [&](int n, int c) -> h8 {
+        if constexpr (kQueriesInLds)
+          return __builtin_bit_cast(h8, sh.q[(n * kSteps + c) * 64 + lane]);
+        else
+          return qreg[n][c];
+      };
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
-        float mx = fmaxf(m[n], fmaf(top[n], f[n], -kBias));
-        mx = fmaxf(mx, __shfl_xor(mx, 16));
-        mx = fmaxf(mx, __shfl_xor(mx, 32));
-        const float down = __builtin_amdgcn_exp2f(m[n] - mx);
-        m[n] = mx;
-        l[n] *= down;
+        m[n] = kNoToken;
+        l[n] = 0.f;
 #pragma unroll
-        for (int d = 0; d < kBlocks; ++d) o[n][d] *= down;
+        for (int j = 0; j < kBlocks; ++j) o[n][j] = f4{0.f, 0.f, 0.f, 0.f};
       }
-    }
-    h8 p[NQ];
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        // (the sum takes p before it is rounded: lse keeps its 32 bits)
-        const float x = __builtin_amdgcn_exp2f(fmaf(sc[e / 4][n][e % 4], f[n], -m[n]));
-        l[n] += x;
-        p[n][e] = static_cast<_Float16>(x);
-      }
-    }
-    values<DIM, NQ>(t, vs, p, o);
-    __builtin_amdgcn_sched_barrier(0);
-    if constexpr (!kTwo) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) load_vals<DIM>(t, h, r.seg[h], lane_at, r.codes[h], r.scales[h]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  };
-  if constexpr (kTwo) {
-    Tile<DIM> u;
-    for (int j = 0; j < mine; j += 2) {
-      step(t, u, j);
-      if (j + 1 >= mine) break;
-      step(u, t, j + 1);
-    }
-  } else {
-    for (int j = 0; j < mine; ++j) step(t, t, j);
-  }
 
-  const AttnParams& z = reread(params);
-  // Join the wavefronts: a row's reference becomes the largest of the four.
+      // The keys of the next tile are on their way during this one's softmax and
+      // values, its values during the next one's scores: one set of registers
+      // each, and the other wavefronts of the SIMD to fill what is left.
+      //
+      // A SIMD serves the older of its wavefronts first, and the workgroup that
+      // came second to a compute unit would end a third later than the first. So
+      // a wavefront's priority falls with every quarter of its tiles: whoever is
+      // behind goes first.
+      const int quarter = (mine + 3) / 4;
+      __builtin_amdgcn_s_setprio(3);
+      // (Where the registers hold two tiles, three row tiles of 128, the whole next
+      // tile is asked for before this one's scores: 57 -> 54 us over 131072 tokens.)
+      constexpr bool kTwo = NQ * DIM == 384;
+      auto step = [&](Tile<DIM>& t, Tile<DIM>& u, int j) {
+        if (j == quarter) __builtin_amdgcn_s_setprio(2);
+        if (j == 2 * quarter) __builtin_amdgcn_s_setprio(1);
+        if (j == 3 * quarter) __builtin_amdgcn_s_setprio(0);
+        const int tok = (t0 + wave + j * kW) * kTileTokens;
+        Place r;
+        bool none0, none1;  // before place(j + 1) looks up the next 64
+        if constexpr (kTwo) {
+          none0 = absent[0] >> (j & 63) & 1, none1 = absent[1] >> (j & 63) & 1;
+          r = place(j + 1);
 #pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    l[n] += __shfl_xor(l[n], 16);
-    l[n] += __shfl_xor(l[n], 32);
-    if (g == 0) ml[wave][n * 16 + i] = float2{m[n], l[n]};
-  }
-  __syncthreads();
-  const int64_t part_rows = static_cast<int64_t>(2 * group_id + (tile0 == 0)) * kRows;
+          for (int h = 0; h < 2; ++h) load_keys<DIM>(u, h, r.seg[h], lane_at, r.codes[h], r.scales[h]);
 #pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    float mx = ml[0][n * 16 + i].x;
-#pragma unroll
-    for (int w = 1; w < kW; ++w) mx = fmaxf(mx, ml[w][n * 16 + i].x);
-    const float down = __builtin_amdgcn_exp2f(m[n] - mx);
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-      for (int d = 0; d < kBlocks; d += 4)
-        *reinterpret_cast<f4*>(&red[wave][i][(g * 4 + r) * kBlocks + d]) =
-            f4{o[n][d][r] * down, o[n][d + 1][r] * down, o[n][d + 2][r] * down, o[n][d + 3][r] * down};
-    __syncthreads();
-    // 8 elements a thread
-    for (int x = tid; x < 16 * DIM / 8; x += kW * 64) {
-      const int r = x / (DIM / 8), d = x % (DIM / 8) * 8, row = n * 16 + r;
-      if (row < nrows) {
-        float mr = ml[0][row].x;
-#pragma unroll
-        for (int w = 1; w < kW; ++w) mr = fmaxf(mr, ml[w][row].x);
-        float lr = 0.f;
-#pragma unroll
-        for (int w = 0; w < kW; ++w) lr += ml[w][row].y * __builtin_amdgcn_exp2f(ml[w][row].x - mr);
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          v[e] = red[0][r][d + e];
-#pragma unroll
-          for (int w = 1; w < kW; ++w) v[e] += red[w][r][d + e];
+          for (int h = 0; h < 2; ++h) load_vals<DIM>(u, h, r.seg[h], lane_at, r.codes[h], r.scales[h]);
+          __builtin_amdgcn_sched_barrier(0);
         }
-        if (!alone) {
-          float* dst = z.part + (part_rows + row) * DIM + d;
-          *reinterpret_cast<f4*>(dst) = f4{v[0], v[1], v[2], v[3]};
-          *reinterpret_cast<f4*>(dst + 4) = f4{v[4], v[5], v[6], v[7]};
-          if (d == 0) {
-            float2* mld = reinterpret_cast<float2*>(z.part + static_cast<int64_t>(2 * z.groups) * kRows * DIM);
-            mld[part_rows + row] = float2{mr, lr};
+        f4 sc[2][NQ];
+        scores<DIM, NQ>(t, query, sc);
+        if constexpr (!kTwo) {
+          none0 = absent[0] >> (j & 63) & 1, none1 = absent[1] >> (j & 63) & 1;
+          __builtin_amdgcn_sched_barrier(0);
+          r = place(j + 1);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) load_keys<DIM>(t, h, r.seg[h], lane_at, r.codes[h], r.scales[h]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        uint32_t vs[2] = {t.vs[0], t.vs[1]};
+        const bool whole =
+            tok + kTileTokens - 1 <= first_pos && (win == 0 || tok > last_pos - win) && !none0 && !none1;
+        if (!whole) {
+          // Scores of unseen tokens become -inf whatever the cache holds there,
+          // and the values of tokens past the end or of absent pages are zeroed:
+          // such bytes may decode to NaN, which a p of 0 would not remove. Bit b
+          // of a mask stands for token tok + 4 g + b.
+          const int mine0 = tok + 4 * g;
+          const auto up_to = [](int x) -> uint32_t { return x < 0 ? 0u : x >= 31 ? ~0u : (2u << x) - 1u; };
+          const uint32_t held = up_to(s.len - 1 - mine0) & ((none0 ? 0u : 0xFFFFu) | (none1 ? 0u : 0xFFFF0000u));
+          const auto bit = [](uint32_t w, int b) {
+            return static_cast<uint32_t>(static_cast<int32_t>(w << (31 - b)) >> 31);
+          };
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) vs[h] &= ~(0xFFu << (8 * e)) | bit(held, 16 * h + e);
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) {
+            // (the row's position is worked out here, for the few tiles that need it)
+            const int pos = s.len - s.ql + (row0 + n * 16 + i) / a.group;
+            const uint32_t seen = held & up_to(pos - mine0) & (win ? ~up_to(pos - win - mine0) : ~0u);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t k = bit(seen, 16 * h + e);
+                sc[h][n][e] = __uint_as_float((__float_as_uint(sc[h][n][e]) & k) | (0xFF800000u & ~k));
+              }
           }
-        } else {
-          const int qi = (row0 + row) / z.group, hh = (row0 + row) - qi * z.group;
-          const int64_t row_at = static_cast<int64_t>(s.qs + qi) * (z.kv_heads * z.group) + head * z.group + hh;
-          const float up = lr > 0.f ? z.v_scale / lr : (lr == 0.f ? 0.f : lr);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] *= up;
-          store_out8<BF16>(z.out, row_at * DIM + d, v);
-          if (d == 0 && z.lse)
-            z.lse[row_at] = lr == 0.f ? -__builtin_inff() : (__builtin_amdgcn_logf(lr) + mr) * 0.69314718055994531f;
         }
+        float far = -__builtin_inff();
+        float top[NQ];
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          top[n] = max3(max3(sc[0][n][0], sc[0][n][1], sc[0][n][2]), sc[0][n][3], sc[1][n][0]);
+          top[n] = max2(max3(top[n], sc[1][n][1], sc[1][n][2]), sc[1][n][3]);
+          far = max2(far, fmaf(top[n], f[n], -m[n]));
+        }
+        if (__any(far > kHeadroom)) {
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) {
+            float mx = fmaxf(m[n], fmaf(top[n], f[n], -kBias));
+            mx = fmaxf(mx, __shfl_xor(mx, 16));
+            mx = fmaxf(mx, __shfl_xor(mx, 32));
+            const float down = __builtin_amdgcn_exp2f(m[n] - mx);
+            m[n] = mx;
+            l[n] *= down;
+#pragma unroll
+            for (int d = 0; d < kBlocks; ++d) o[n][d] *= down;
+          }
+        }
+        h8 p[NQ];
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            // (the sum takes p before it is rounded: lse keeps its 32 bits)
+            const float x = __builtin_amdgcn_exp2f(fmaf(sc[e / 4][n][e % 4], f[n], -m[n]));
+            l[n] += x;
+            p[n][e] = static_cast<_Float16>(x);
+          }
+        }
+        values<DIM, NQ>(t, vs, p, o);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (!kTwo) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) load_vals<DIM>(t, h, r.seg[h], lane_at, r.codes[h], r.scales[h]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      };
+      if constexpr (kTwo) {
+        Tile<DIM> u;
+        for (int j = 0; j < mine; j += 2) {
+          step(t, u, j);
+          if (j + 1 >= mine) break;
+          step(u, t, j + 1);
+        }
+      } else {
+        for (int j = 0; j < mine; ++j) step(t, t, j);
+      }
+
+      const AttnParams& z = reread(params);
+      // Join the wavefronts: a row's reference becomes the largest of the four.
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        l[n] += __shfl_xor(l[n], 16);
+        l[n] += __shfl_xor(l[n], 32);
+        if (g == 0) ml[wave][n * 16 + i] = float2{m[n], l[n]};
+      }
+      __syncthreads();
+      const int64_t part_rows = static_cast<int64_t>(2 * group_id + (tile0 == 0)) * kRows;
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        float mx = ml[0][n * 16 + i].x;
+#pragma unroll
+        for (int w = 1; w < kW; ++w) mx = fmaxf(mx, ml[w][n * 16 + i].x);
+        const float down = __builtin_amdgcn_exp2f(m[n] - mx);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int d = 0; d < kBlocks; d += 4)
+            *reinterpret_cast<f4*>(&red[wave][i][(g * 4 + r) * kBlocks + d]) =
+                f4{o[n][d][r] * down, o[n][d + 1][r] * down, o[n][d + 2][r] * down, o[n][d + 3][r] * down};
+        __syncthreads();
+        // 8 elements a thread
+        for (int x = tid; x < 16 * DIM / 8; x += kW * 64) {
+          const int r = x / (DIM / 8), d = x % (DIM / 8) * 8, row = n * 16 + r;
+          if (row < nrows) {
+            float mr = ml[0][row].x;
+#pragma unroll
+            for (int w = 1; w < kW; ++w) mr = fmaxf(mr, ml[w][row].x);
+            float lr = 0.f;
+#pragma unroll
+            for (int w = 0; w < kW; ++w) lr += ml[w][row].y * __builtin_amdgcn_exp2f(ml[w][row].x - mr);
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              v[e] = red[0][r][d + e];
+#pragma unroll
+              for (int w = 1; w < kW; ++w) v[e] += red[w][r][d + e];
+            }
+            if (!alone) {
+              float* dst = z.part + (part_rows + row) * DIM + d;
+              *reinterpret_cast<f4*>(dst) = f4{v[0], v[1], v[2], v[3]};
+              *reinterpret_cast<f4*>(dst + 4) = f4{v[4], v[5], v[6], v[7]};
+              if (d == 0) {
+                float2* mld = reinterpret_cast<float2*>(z.part + static_cast<int64_t>(2 * z.groups) * kRows * DIM);
+                mld[part_rows + row] = float2{mr, lr};
+              }
+            } else {
+              const int qi = (row0 + row) / z.group, hh = (row0 + row) - qi * z.group;
+              const int64_t row_at = static_cast<int64_t>(s.qs + qi) * (z.kv_heads * z.group) + head * z.group + hh;
+              const float up = lr > 0.f ? z.v_scale / lr : (lr == 0.f ? 0.f : lr);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] *= up;
+              store_out8<BF16>(z.out, row_at * DIM + d, v);
+              if (d == 0 && z.lse)
+                z.lse[row_at] = lr == 0.f ? -__builtin_inff() : (__builtin_amdgcn_logf(lr) + mr) * 0.69314718055994531f;
+            }
+          }
+        }
+        __syncthreads();
       }
     }
-    __syncthreads();
-  }
-  }
-  if (at >= end) break;
-  if (at - base >= cost * s.rt * reread(params).kv_heads) {
-    // the next sequence that has rows
-    base = at;
-    do seq = sequence(reread(params), ++b, kRows);
-    while (seq.rt == 0);
-  }
+    if (at >= end) break;
+    if (at - base >= cost * s.rt * reread(params).kv_heads) {
+      // the next sequence that has rows
+      base = at;
+      do seq = sequence(reread(params), ++b, kRows);
+      while (seq.rt == 0);
+    }
   }
 }
 

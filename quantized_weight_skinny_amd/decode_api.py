@@ -41,6 +41,15 @@ HALVES = (torch.float16, torch.bfloat16)
 # counts: checks compare plain attributes, the descriptors of a cache are built
 # once, and the current stream is taken as the raw handle that torch keeps.
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
+def _stream(device):
+    """The device's current stream. A kernel runs on the current device, so that
+    must be the tensors'."""
+    if _current_device() != device.index:
+        raise ValueError(f"the tensors are on {device}, which is not the current device: call under torch.cuda.device")
+    return _raw_stream(device.index)
 
 
 def _on_device(t, name, device=None):
@@ -163,7 +172,7 @@ def kv4_append(cache, k, v, slots, layer=0):
     vp, vt, vh = _rows(v, shape, "v", dev, (k.dtype,))
     sp = _exactly(slots, torch.int64, (tokens,), "slots", dev)
     qpn_kv4_append(cache.desc(layer), layer, kp, vp, DTYPES[k.dtype], tokens, kt, kh, vt, vh, sp,
-                   _raw_stream(dev.index))
+                   _stream(dev))
 
 
 def kv4_read(cache, slots, layer=0, dtype=torch.float16, k=None, v=None):
@@ -178,7 +187,7 @@ def kv4_read(cache, slots, layer=0, dtype=torch.float16, k=None, v=None):
     k = _out(k, dtype, shape, "k", dev)
     v = _out(v, dtype, shape, "v", dev)
     qpn_kv4_read(cache.desc(layer), layer, sp, tokens, DTYPES[dtype], k.data_ptr(), v.data_ptr(),
-                 _raw_stream(dev.index))
+                 _stream(dev))
     return k, v
 
 
@@ -190,7 +199,7 @@ def kv4_copy_pages(cache, src, dst):
     n = src.shape[0]
     sp = _exactly(src, torch.int32, (n,), "src", dev)
     dp = _exactly(dst, torch.int32, (n,), "dst", dev)
-    qpn_kv4_copy_pages(cache.desc(), sp, dp, n, _raw_stream(dev.index))
+    qpn_kv4_copy_pages(cache.desc(), sp, dp, n, _stream(dev))
 
 
 @functools.lru_cache(maxsize=256)
@@ -257,7 +266,7 @@ def kv4_attention(q, cache, table, kv_len, q_start=None, max_q_len=None, max_kv_
     workspace, wp, nbytes = _workspace(
         _attention_workspace_bytes(cache.page_size, kv_heads, dim, rows, heads, batch, max_q_len, max_kv_len), workspace,
         dev)
-    qpn_kv4_attention(cache.desc(layer), a, wp, nbytes, _raw_stream(dev.index))
+    qpn_kv4_attention(cache.desc(layer), a, wp, nbytes, _stream(dev))
     return out, lse
 
 
@@ -311,5 +320,5 @@ def verify_drafts(target, draft_tokens, u_accept, u_sample, draft=None, num_draf
                         accepted.data_ptr(), logprobs.data_ptr(), tb, tr, db, dr, DTYPES[target.dtype],
                         1 if probabilities else 0, batch, drafts, vocab, 0)
     workspace, wp, nbytes = _workspace(_verify_workspace_bytes(batch, drafts, vocab), workspace, dev)
-    qpn_verify(a, wp, nbytes, _raw_stream(dev.index))
+    qpn_verify(a, wp, nbytes, _stream(dev))
     return tokens, accepted, logprobs

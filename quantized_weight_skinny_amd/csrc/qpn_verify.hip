@@ -40,6 +40,35 @@ struct Stat {
 };
 static_assert(sizeof(Stat) == 16, "the workspace holds 16 bytes a chunk");
 
+// Running sums over a wavefront's lanes by data-parallel moves (lane l gets
+// the value of lane l - n of its row of 16, then of the rows before): six
+// steps of three instructions, against two trips through LDS each for a
+// shuffled 64-bit value.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double moved(double x) {
+  const long long b = __builtin_bit_cast(long long, x);
+  const int lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(b), CTRL, ROWS, 0xF, false);
+  const int hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(b >> 32), CTRL, ROWS, 0xF, false);
+  return __builtin_bit_cast(double, static_cast<unsigned long long>(static_cast<uint32_t>(hi)) << 32 |
+                                        static_cast<uint32_t>(lo));
+}
+__device__ __forceinline__ double wave_scan(double x) {
+  x += moved<0x111, 0xF>(x);  // one lane up in the row
+  x += moved<0x112, 0xF>(x);  // two
+  x += moved<0x114, 0xF>(x);  // four
+  x += moved<0x118, 0xF>(x);  // eight
+  x += moved<0x142, 0xA>(x);  // the last lane of rows 0 and 2, to rows 1 and 3
+  x += moved<0x143, 0xC>(x);  // lane 31, to rows 2 and 3
+  return x;
+}
+__device__ __forceinline__ double lane_value(double x, int l) {
+  const long long b = __builtin_bit_cast(long long, x);
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(b), l);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(b >> 32), l);
+  return __builtin_bit_cast(double, static_cast<unsigned long long>(hi) << 32 | lo);
+}
+__device__ __forceinline__ double wave_sum(double x) { return lane_value(wave_scan(x), 63); }
+
 // What the accept tests leave to the passes that draw a token.
 enum : int { kDone = 0, kFromP = 1, kFromRest = 2 };
 struct Verdict {
@@ -162,9 +191,7 @@ __device__ __forceinline__ Stat join_stats(const Stat* s, int chunks, float scal
   const float mine = r.max;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) fold_max(r.max, r.idx, o);
-  r.sum *= ratio(mine, r.max);
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) r.sum += __shfl_xor(r.sum, o);
+  r.sum = wave_sum(r.sum * ratio(mine, r.max));
   return r;
 }
 
@@ -179,9 +206,23 @@ __device__ Verdict decide(const VerifyParams& p, int b, bool write) {
   const float t = PROBS ? 1.f : temperature_of(p, b);
   const int tid = threadIdx.x, places = p.a.drafts + 1;
   const double inv_t = 1.0 / (t > 0.f ? t : 1.f);
+  // a draft's token, its logits and its number are on their way while the rows are joined
+  const bool with_q = p.a.draft && t > 0.f;  // (a greedy sequence has no use for the draft's rows)
+  int d = -1;
+  float u = 0.f;
+  float x_p = 0.f, x_q = 0.f;
+  if (tid < n) {
+    const int64_t at = static_cast<int64_t>(b) * p.a.drafts + tid;
+    d = p.a.draft_tokens[at];
+    u = p.a.u_accept[at];
+    if (d >= 0 && d < p.a.vocab) {
+      x_p = widen<T>(target_row<T>(p, b, tid)[d]);
+      if (with_q) x_q = widen<T>(draft_row<T>(p, b, tid)[d]);
+    }
+  }
   if constexpr (!PROBS) {
     const float scale = 1.44269504088896341f / (t > 0.f ? t : 1.f);
-    const int rows = n + 1 + (p.a.draft && t > 0.f ? n : 0);
+    const int rows = n + 1 + (with_q ? n : 0);
 #pragma unroll 1
     for (int r = tid >> 6; r < rows; r += kDrawWaves) {
       const int64_t row = r <= n ? static_cast<int64_t>(b) * places + r
@@ -193,31 +234,27 @@ __device__ Verdict decide(const VerifyParams& p, int b, bool write) {
   }
   if (tid == 0) rejected_at = n;
   __syncthreads();
-  int d = -1;
-  double pd = 0.0;   // p of the draft
+  double pd = 0.0;  // p of the draft
   if (tid < n) {
-    const int64_t at = static_cast<int64_t>(b) * p.a.drafts + tid;
-    d = p.a.draft_tokens[at];
     bool ok = false;
     if (d >= 0 && d < p.a.vocab) {
       double qd = 1.0;
-      int best = -1;
-      // p, then q where the draft has rows (a greedy sequence has no use for it)
 #pragma unroll 1
-      for (int k = 0; k < (p.a.draft && t > 0.f ? 2 : 1); ++k) {
-        const T x = (k ? draft_row<T>(p, b, tid) : target_row<T>(p, b, tid))[d];
+      for (int k = 0; k < (with_q ? 2 : 1); ++k) {
+        const float x = k ? x_q : x_p;
         double y;
         if constexpr (PROBS) {
-          y = probability(widen<T>(x));
+          y = probability(x);
         } else {
           const Stat r = (k ? q_rows : p_rows)[tid];
-          y = r.sum > 0.0 ? weight(logit<T>(x), r.max, inv_t) / r.sum : 0.0;
-          if (k == 0) best = r.idx;
+          y = r.sum > 0.0 ? weight(x == x ? x : -__builtin_inff(), r.max, inv_t) / r.sum : 0.0;
         }
         if (k) qd = y;
         else pd = y;
       }
-      ok = !PROBS && t == 0.f ? best == d : static_cast<double>(p.a.u_accept[at]) * qd < pd;
+      ok = static_cast<double>(u) * qd < pd;
+      if constexpr (!PROBS)
+        if (t == 0.f) ok = p_rows[tid].idx == d;
     }
     if (!ok) atomicMin(&rejected_at, tid);
   }
@@ -314,9 +351,7 @@ __global__ __launch_bounds__(kT) void verify_rows_kernel(const VerifyParams p, i
     const float w = x[e] == m ? 1.f : __builtin_amdgcn_exp2f((x[e] - m) * scale);
     s += x[e] == -__builtin_inff() ? 0.f : w;
   }
-  double sum = s;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o);
+  double sum = wave_sum(s);
   if ((threadIdx.x & 63) == 0) wsum[threadIdx.x >> 6] = sum;
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -329,24 +364,12 @@ __global__ __launch_bounds__(kT) void verify_rows_kernel(const VerifyParams p, i
 
 // Two sums over the workgroup, to every thread.
 __device__ __forceinline__ void block_sum2(double& a, double& b, double (&buf)[kDrawWaves][2]) {
-#pragma unroll 1
-  for (int o = 1; o < 64; o <<= 1) a += __shfl_xor(a, o), b += __shfl_xor(b, o);
+  a = wave_sum(a), b = wave_sum(b);
   if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6][0] = a, buf[threadIdx.x >> 6][1] = b;
   __syncthreads();
   a = b = 0.0;
 #pragma unroll 4
   for (int w = 0; w < kDrawWaves; ++w) a += buf[w][0], b += buf[w][1];
-}
-
-// Inclusive running sum over a wavefront's lanes.
-__device__ __forceinline__ double wave_scan(double x) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll 1
-  for (int o = 1; o < 64; o <<= 1) {
-    const double y = __shfl_up(x, o);
-    if (lane >= o) x += y;
-  }
-  return x;
 }
 
 // The weights of this thread's places e0 + j * step of the row that a token is
@@ -475,10 +498,8 @@ __global__ __launch_bounds__(kD) void verify_pick_kernel(const VerifyParams p) {
         z[2] += sums[2 * p.chunks + j];
       }
     }
-#pragma unroll 1
-    for (int o = 1; o < 64; o <<= 1)
 #pragma unroll
-      for (int k = 0; k < 3; ++k) z[k] += __shfl_xor(z[k], o);
+    for (int k = 0; k < 3; ++k) z[k] = wave_sum(z[k]);
     const bool rest = qr && z[2] > 0.0;  // nothing left over: from p
     const double* cs = rest ? sums + 2 * p.chunks : sums;
     const double aim = static_cast<double>(u) * (rest ? z[2] : z[0]);
@@ -494,11 +515,11 @@ __global__ __launch_bounds__(kD) void verify_pick_kernel(const VerifyParams p) {
       if (over) {
         const int l = __builtin_ctzll(over);
         chunk = j0 + l;
-        before = __shfl(sum - x, l);
+        before = lane_value(sum - x, l);
         break;
       }
       if (some) chunk = j0 + 63 - __builtin_clzll(some);
-      run = __shfl(sum, 63);
+      run = lane_value(sum, 63);
     }
     if (lane == 0) {
       s_chunk = chunk;
@@ -526,8 +547,8 @@ __global__ __launch_bounds__(kD) void verify_pick_kernel(const VerifyParams p) {
     if (lane == 63) wsum[wave] = sum;
     __syncthreads();
     sum -= mine;
-#pragma unroll 1
-    for (int k = 0; k < wave; ++k) sum += wsum[k];
+#pragma unroll
+    for (int k = 0; k < kDrawWaves - 1; ++k) sum += k < wave ? wsum[k] : 0.0;
     int hit = 0x7FFFFFFF, end = -1;
 #pragma unroll
     for (int j = 0; j < kDrawPer; ++j) {
@@ -538,8 +559,11 @@ __global__ __launch_bounds__(kD) void verify_pick_kernel(const VerifyParams p) {
         if (sum > s_left && hit == 0x7FFFFFFF) hit = end;
       }
     }
-    if (hit != 0x7FFFFFFF) atomicMin(&found, hit);
-    if (end >= 0) atomicMax(&last, end);
+    // lanes lie in order: one of each wavefront speaks for it (1024 atomics on
+    // one place took 6 us)
+    const unsigned long long hits = __ballot(hit != 0x7FFFFFFF), ends = __ballot(end >= 0);
+    if (hits && lane == static_cast<int>(__builtin_ctzll(hits))) atomicMin(&found, hit);
+    if (ends && lane == 63 - static_cast<int>(__builtin_clzll(ends))) atomicMax(&last, end);
     __syncthreads();
     token = chunk * kChunk + (found != 0x7FFFFFFF ? found : last);
   }

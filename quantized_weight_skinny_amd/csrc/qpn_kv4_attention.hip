@@ -907,7 +907,8 @@ hipError_t launch_kv4_attention(const qpn_kv4_cache& c, const qpn_kv4_attention_
   a.table = x.table, a.table_stride = x.table_stride;
   a.kv_len = x.kv_len, a.q_start = x.q_start;
   a.batch = x.batch, a.rows = x.rows, a.max_q = x.max_q_len < x.rows ? x.max_q_len : x.rows;
-  a.max_kv = x.max_kv_len, a.window = x.window;
+  // (no length is above 2^30; a position less the window stays inside 32 bits)
+  a.max_kv = x.max_kv_len, a.window = x.window < (1 << 30) ? x.window : 1 << 30;
   a.row_tiles = p.row_tiles, a.groups = p.groups, a.min_share = p.min_share;
   a.f = x.scale * 1.44269504088896341f * c.k_scale;
   a.v_scale = c.v_scale;

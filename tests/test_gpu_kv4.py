@@ -266,6 +266,15 @@ def test_attention_window(window):
     c.check(c.run(window=window), window)
 
 
+@pytest.mark.parametrize("window", [1 << 30, (1 << 31) - 1])
+def test_attention_window_as_wide_as_its_type_hides_nothing(window):
+    """Also where rows lie before the sequence's start, so that a position less the window is lowest."""
+    c = Case(21, [4, 0, 40, 600], [16, 5, 9, 16], 6, 2, 64, 16, "fp16")
+    got, want = c.run(window=window), c.run(window=0)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    c.check(got)
+
+
 def test_attention_empty_rows():
     """Lengths of zero, blocks longer than their sequence (rows before its
     start) and sequences without rows."""

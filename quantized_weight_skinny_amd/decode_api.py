@@ -36,6 +36,7 @@ from .page_pool import OutOfPages, PagePool  # noqa: F401  (part of this module'
 
 DTYPES = {torch.float16: QPN_DT_F16, torch.bfloat16: QPN_DT_BF16, torch.float32: QPN_DT_F32}
 HALVES = (torch.float16, torch.bfloat16)
+INT32_MAX = 2**31 - 1  # ctypes cuts a larger number to its low 32 bits without a word
 
 # A verify step makes these calls once a layer, so what Python adds to each
 # counts: checks compare plain attributes, the descriptors of a cache are built
@@ -258,6 +259,8 @@ def kv4_attention(q, cache, table, kv_len, q_start=None, max_q_len=None, max_kv_
         max_q_len = each
     if max_kv_len is None:
         max_kv_len = held * cache.page_size
+    if not (0 <= window <= INT32_MAX and 0 <= max_q_len <= INT32_MAX and 0 <= max_kv_len <= INT32_MAX):
+        raise ValueError(f"window {window}, max_q_len {max_q_len} and max_kv_len {max_kv_len} must be 0 .. {INT32_MAX}")
     out = _out(out, q.dtype, (rows, heads, dim), "out", dev)
     lse = _out(lse, torch.float32, (rows, heads), "lse", dev)
     a = qpn_kv4_attention_args(qp, out.data_ptr(), lse.data_ptr(), table.data_ptr(), lp, sp, qt, qh,
@@ -311,6 +314,8 @@ def verify_drafts(target, draft_tokens, u_accept, u_sample, draft=None, num_draf
         if probabilities:
             raise ValueError("probabilities are taken as they are: no temperature")
         tmp = _exactly(temperature, torch.float32, (batch,), "temperature", dev)
+    if vocab > INT32_MAX:
+        raise ValueError(f"a vocabulary of {vocab} is more than {INT32_MAX}")
     tokens = _out(tokens, torch.int32, (batch, places), "tokens", dev)
     accepted = _out(accepted, torch.int32, (batch,), "accepted", dev)
     logprobs = _out(logprobs, torch.float32, (batch, places), "logprobs", dev)

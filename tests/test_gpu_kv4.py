@@ -275,6 +275,13 @@ def test_attention_window_as_wide_as_its_type_hides_nothing(window):
     c.check(got)
 
 
+def test_attention_refuses_numbers_beyond_32_bits():
+    c = Case(22, [40], [2], 2, 1, 64, 16, "fp16")
+    for kw in (dict(window=(1 << 32) + 7), dict(window=-1), dict(max_kv_len=(1 << 32) + 40), dict(max_kv_len=-1)):
+        with pytest.raises(ValueError, match="must be 0"):
+            c.run(**kw)
+
+
 def test_attention_empty_rows():
     """Lengths of zero, blocks longer than their sequence (rows before its
     start) and sequences without rows."""

@@ -85,7 +85,9 @@ __device__ __forceinline__ uint2 load_block(const BlockRef& r) {
 // an element would be a third of the kernel's instructions, so the block
 // divides once: with r = 1 / d correctly rounded and q = x * r, off by at most
 // an ulp, q + (x - q d) r, the residual exact in a fused multiply-add, is the
-// correctly rounded x / d. Blocks with an infinity or NaN take the division.
+// correctly rounded x / d. (Where x r overflows the correction gives NaN, which
+// the conversion takes to the largest code, as it does an infinite quotient.)
+// Blocks with an infinity or NaN take the division.
 // 16389 tokens of 2 x 1024 elements: 37 us with divisions and a comparison
 // for every midpoint, 21 us so (4.1 TB/s of values in and codes out).
 template <bool BF16>

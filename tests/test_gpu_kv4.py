@@ -179,6 +179,29 @@ def test_append_rounds_division_like_ieee(dim):
         assert np.all(np.abs(to_host(got.double()) - want) <= np.abs(want) * 2.0 ** -23)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("scales", [(0.001, 2.0 ** -50), (2.0 ** -70, 2.0 ** 70), (2.0 ** 59, 1.0)])
+def test_append_values_at_the_end_of_bf16(dim, scales):
+    """Magnitudes up to 2^127 and down to bf16's smallest, beside each other:
+    quotients that leave fp32 count as infinite, those that vanish as zeros."""
+    say("append extremes", dim, scales)
+    rng = np.random.default_rng(dim)
+    tokens, page, kvh = 48, 16, 2
+    x = rng.standard_normal((tokens, 2 * kvh, dim)) * 2.0 ** rng.uniform(-133, 126, (tokens, 2 * kvh, dim))
+    x[0::3] = rng.standard_normal((tokens // 3, 2 * kvh, dim)) * 2.0 ** 125
+    x[1::3] = rng.standard_normal((tokens // 3, 2 * kvh, dim)) * 2.0 ** rng.uniform(-130, 120, (tokens // 3, 2 * kvh, 1))
+    xd = torch.from_numpy(x.astype(np.float32)).to(torch.bfloat16)
+    cache = qd.KV4Cache(tokens // page, page, kvh, dim, k_scale=scales[0], v_scale=scales[1])
+    ref = to_host(cache.data).copy()
+    qd.kv4_append(cache, xd[:, :kvh].to(DEV), xd[:, kvh:].to(DEV), torch.arange(tokens, dtype=torch.int64, device=DEV))
+    f = xd.float().numpy()
+    with np.errstate(all="ignore"):
+        for t in range(tokens):
+            ok.kv4_store(ref[0], page, kvh, dim, t, ok.kv4_quantize(f[t, :kvh], scales[0]),
+                         ok.kv4_quantize(f[t, kvh:], scales[1]))
+    assert np.array_equal(to_host(cache.data), ref)
+
+
 def test_append_unaligned_rows():
     say("append unaligned")
     rng = np.random.default_rng(3)

@@ -151,6 +151,8 @@ class PagePool:
         return page
 
     def _copy(self, src, dst):
+        # a page whose own copy is still to be made is read where that reads
+        src = next((s for s, d in self._copies if d == src), src)
         self._copies.append((src, dst))
         self._copied.update((src, dst))
 

@@ -120,6 +120,20 @@ def test_pages_of_pending_copies_are_not_taken_again():
     assert p.free_pages == 4
 
 
+def test_a_copy_of_a_page_whose_own_copy_is_pending_reads_the_first():
+    p = PagePool(8, 4)
+    a = p.new()
+    p.extend(a, 2)
+    b = p.fork(a)
+    p.extend(b, 1)                       # a's page -> b's is pending
+    p.truncate(b, 2)
+    c = p.fork(b)
+    p.extend(c, 1)                       # b's page holds nothing yet: c's copy is of a's
+    x, y, z = (p.table(s)[0] for s in (a, b, c))
+    assert len({x, y, z}) == 3
+    assert sorted(p.take_copies()) == sorted([(x, y), (x, z)])
+
+
 def test_full_last_page_is_not_copied():
     p = PagePool(8, 4)
     a = p.new()

@@ -117,9 +117,10 @@ class PagePool:
 
     def compact(self):
         """Moves the pages in use to the lowest indices (each into a hole below
-        it), so that the pool's end is free. Adds the moves to the copies and
-        returns the number of pages in use. Copies must have been taken first:
-        a page may not be a source and a destination at once."""
+        it), so that the pool's end is free once the copies have been taken.
+        Adds the moves to the copies and returns the number of pages in use.
+        Copies must have been taken before, too: a page may not be a source
+        and a destination at once."""
         if self._copies:
             raise RuntimeError("take_copies() first: a move must not meet a copy that is still to be made")
         used = self.pages - len(self._free)
@@ -131,7 +132,8 @@ class PagePool:
             self._refs[dst], self._refs[src] = self._refs[src], 0
         for held in self._held.values():
             held[:] = [to.get(p, p) for p in held]
-        self._free = list(range(self.pages - 1, used - 1, -1))
+        self._free = [p for p in range(self.pages - 1, used - 1, -1) if p not in to]
+        self._late = list(to)            # free once they have been read
         return used
 
     def take_copies(self):

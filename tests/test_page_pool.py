@@ -134,6 +134,22 @@ def test_a_copy_of_a_page_whose_own_copy_is_pending_reads_the_first():
     assert sorted(p.take_copies()) == sorted([(x, y), (x, z)])
 
 
+def test_pages_that_compact_empties_are_not_taken_before_its_moves_are_made():
+    p = PagePool(6, 4)
+    a, b = p.new(), p.new()
+    p.extend(a, 16)
+    p.extend(b, 6)                       # pages 4 and 5
+    p.truncate(a, 8)
+    assert p.compact() == 4              # 4 and 5 move to 2 and 3
+    assert p.table(b) == [2, 3]
+    c = p.fork(b)
+    with pytest.raises(OutOfPages):
+        p.extend(c, 1)                   # its copy would be written into a page that a move reads
+    p.take_copies()
+    p.extend(c, 1)
+    assert p.take_copies() == [(3, p.table(c)[1])] and p.free_pages == 1
+
+
 def test_full_last_page_is_not_copied():
     p = PagePool(8, 4)
     a = p.new()

@@ -34,7 +34,7 @@
 // counts to 1600 cycles a SIMD; 1670 are measured, with two wavefronts, which
 // a SIMD needs: one alone issues a vector instruction every 8 cycles, two or
 // more every 4 to 5. So 131072 tokens of 8 heads (151 MB) take 27 us of vector
-// instructions against 25 us of memory, and the call 50: the rest is the
+// instructions against 25 us of memory, and the call 47: the rest is the
 // launch (2), the shares' counting and first loads (6), joining wavefronts (3)
 // and pieces (6), and what memory's latency leaves open. At one row tile (one
 // row, four wavefronts a SIMD) 24 sequences' 180 MB take 39 us.

@@ -425,6 +425,17 @@ __device__ __forceinline__ void weights(const VerifyParams& p, const Verdict& v,
   }
 }
 
+// What the draft leaves over of a token, from weights and factors. Both products
+// are rounded before the difference: in a fused multiply-add one of them would
+// not be, and where the rows agree the rounding of the other would be left over,
+// to be drawn from instead of p. The sums and the pick call this one function, so
+// that a chunk whose sum is above 0 has a token whose share is.
+__device__ __forceinline__ double left_over(double wp, double scale_p, double wq, double scale_q) {
+#pragma clang fp contract(off)
+  const double p = wp * scale_p, q = wq * scale_q;
+  return fmax(p - q, 0.0);
+}
+
 // The accept tests alone, a workgroup a sequence.
 template <typename T>
 __global__ __launch_bounds__(kD) void verify_decide_kernel(const VerifyParams p) {
@@ -459,10 +470,10 @@ __global__ __launch_bounds__(kD) void verify_sums_kernel(const VerifyParams p) {
 #pragma unroll
   for (int j = 0; j < kDrawPer; ++j) {
     if constexpr (REST) {
-      sp += fmax(wp[j] * scale_p - wq[j] * scale_q, 0.0);
+      sp += left_over(wp[j], scale_p, wq[j], scale_q);
     } else {
       sp += wp[j];
-      sq += PROBS ? fmax(wp[j] - wq[j], 0.0) : wq[j];
+      sq += PROBS ? left_over(wp[j], 1.0, wq[j], 1.0) : wq[j];
     }
   }
   block_sum2(sp, sq, buf);
@@ -543,7 +554,7 @@ __global__ __launch_bounds__(kD) void verify_pick_kernel(const VerifyParams p) {
     double wp[kDrawPer], wq[kDrawPer];
     weights<T, PROBS, true>(p, v, pr, s_rest ? qr : nullptr, chunk * kChunk + tid, kD, wp, wq);
 #pragma unroll
-    for (int j = 0; j < kDrawPer; ++j) w[j * kD + tid] = fmax(wp[j] * s_scale_p - wq[j] * s_scale_q, 0.0);
+    for (int j = 0; j < kDrawPer; ++j) w[j * kD + tid] = left_over(wp[j], s_scale_p, wq[j], s_scale_q);
     __syncthreads();
     double mine = 0.0;
 #pragma unroll

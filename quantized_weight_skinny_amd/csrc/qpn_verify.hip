@@ -458,7 +458,7 @@ __global__ __launch_bounds__(kD) void verify_sums_kernel(const VerifyParams p) {
   weights<T, PROBS, false>(p, v, pr, qr, c * kChunk + threadIdx.x, kD, wp, wq);
   double scale_p = 1.0, scale_q = 1.0;
   if constexpr (REST) {
-    double zp = 0.0, zq = 0.0;
+    double zp = 0.0, zq = 0.0;  // (verify_pick_kernel adds them in the same order)
 #pragma unroll 1
     for (int j = threadIdx.x; j < p.chunks; j += kD) zp += sums[j], zq += sums[p.chunks + j];
     block_sum2(zp, zq, buf);
@@ -504,18 +504,25 @@ __global__ __launch_bounds__(kD) void verify_pick_kernel(const VerifyParams p) {
   if (wave == 0) {
     const double* sums = p.sums + static_cast<int64_t>(b) * 3 * p.chunks;
     const float u = p.a.u_sample[b];
-    // the totals of p, q and of what is left over
+    // the totals of p, q and of what is left over, those of p and q in the order
+    // of the pass that summed that (a thread's places, lanes, wavefronts): with
+    // totals of another order all that rounding left of a chunk there could be
+    // gone here
     double z[3] = {0.0, 0.0, 0.0};
 #pragma unroll 1
-    for (int j = lane; j < p.chunks; j += 64) {
-      z[0] += sums[j];
-      if (qr) {
-        if constexpr (!PROBS) z[1] += sums[p.chunks + j];
-        z[2] += sums[2 * p.chunks + j];
+    for (int w0 = 0; w0 < min(p.chunks, kD); w0 += 64) {
+      double x[3] = {0.0, 0.0, 0.0};
+#pragma unroll 1
+      for (int j = w0 + lane; j < p.chunks; j += kD) {
+        x[0] += sums[j];
+        if (qr) {
+          if constexpr (!PROBS) x[1] += sums[p.chunks + j];
+          x[2] += sums[2 * p.chunks + j];
+        }
       }
-    }
 #pragma unroll
-    for (int k = 0; k < 3; ++k) z[k] = wave_sum(z[k]);
+      for (int k = 0; k < 3; ++k) z[k] += wave_sum(x[k]);
+    }
     const bool rest = qr && z[2] > 0.0;  // nothing left over: from p
     const double* cs = rest ? sums + 2 * p.chunks : sums;
     const double aim = static_cast<double>(u) * (rest ? z[2] : z[0]);

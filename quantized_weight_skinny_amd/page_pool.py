@@ -33,8 +33,8 @@ class PagePool:
         self._held = {}                               # sequence -> [page, ...]
         self._len = {}
         self._next = 0
-        self._copies = []
-        self._copied = set()                          # pages of copies that are still to be made,
+        self._copies = {}                             # destination -> source, of copies still to be made
+        self._copied = set()                          # their pages,
         self._late = []                               # and those of them that nobody holds any more
 
     # ------------------------------------------------------------- queries
@@ -139,7 +139,8 @@ class PagePool:
     def take_copies(self):
         """The (source, destination) pairs to be made before anything is written
         to the pool again; afterwards none are pending."""
-        out, self._copies = self._copies, []
+        out = [(src, dst) for dst, src in self._copies.items()]
+        self._copies.clear()
         self._copied.clear()
         self._free += self._late
         self._late = []
@@ -154,8 +155,8 @@ class PagePool:
 
     def _copy(self, src, dst):
         # a page whose own copy is still to be made is read where that reads
-        src = next((s for s, d in self._copies if d == src), src)
-        self._copies.append((src, dst))
+        src = self._copies.get(src, src)
+        self._copies[dst] = src
         self._copied.update((src, dst))
 
     def _drop(self, page):

@@ -41,7 +41,7 @@ class Decoder:
         self.embed = torch.randn((vocab, hidden), device=device, generator=gen).half()
         self.cache = qd.KV4Cache(pages, page_size, kv_heads, dim, layers, k_scale=5.0 / 2688, v_scale=5.0 / 2688,
                                  device=device)
-        self.pool = qd.PagePool(pages, page_size)
+        self.pool = qd.PagePool(pages, page_size, track_writes=True)
 
     @staticmethod
     def norm(x):
@@ -70,6 +70,7 @@ class Decoder:
             a, _ = qd.kv4_attention(q, self.cache, table, kv_len, layer=i)
             x = x + qt.gemm(a.view(rows, q_size), w["out"])
             x = x + qt.mlp(self.norm(x), w["up"], w["down"])[1]
+        self.pool.written(seq)
         return qt.gemm(self.norm(x), self.head)
 
 

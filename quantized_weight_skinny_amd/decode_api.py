@@ -32,7 +32,7 @@ from .decode import (
     qpn_verify_args,
     qpn_verify_workspace_bytes,
 )
-from .page_pool import OutOfPages, PagePool  # noqa: F401  (part of this module's interface)
+from .page_pool import NotWritten, OutOfPages, PagePool  # noqa: F401  (part of this module's interface)
 
 DTYPES = {torch.float16: QPN_DT_F16, torch.bfloat16: QPN_DT_BF16, torch.float32: QPN_DT_F32}
 HALVES = (torch.float16, torch.bfloat16)

@@ -99,6 +99,8 @@ def _workspace(need, workspace, device):
         return None, None, 0
     if workspace is not None:
         _on_device(workspace, "workspace", device)
+        if not workspace.is_contiguous():   # its elements would not be its bytes
+            raise ValueError("workspace must be contiguous")
         have = workspace.numel() * workspace.element_size()
         if have >= need:
             return workspace, workspace.data_ptr(), have

@@ -263,6 +263,8 @@ def kv4_attention(q, cache, table, kv_len, q_start=None, max_q_len=None, max_kv_
         max_kv_len = held * cache.page_size
     if not (0 <= window <= INT32_MAX and 0 <= max_q_len <= INT32_MAX and 0 <= max_kv_len <= INT32_MAX):
         raise ValueError(f"window {window}, max_q_len {max_q_len} and max_kv_len {max_kv_len} must be 0 .. {INT32_MAX}")
+    if max_kv_len > held * cache.page_size:   # (a slice's rows may lie further apart than they are long)
+        raise ValueError(f"max_kv_len {max_kv_len} is more than a table row's {held} pages of {cache.page_size} hold")
     out = _out(out, q.dtype, (rows, heads, dim), "out", dev)
     lse = _out(lse, torch.float32, (rows, heads), "lse", dev)
     a = qpn_kv4_attention_args(qp, out.data_ptr(), lse.data_ptr(), table.data_ptr(), lp, sp, qt, qh,

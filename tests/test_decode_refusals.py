@@ -26,3 +26,17 @@ def test_a_workspace_must_be_contiguous(on_host):
     assert qd._workspace(4096, ws, CPU) == (ws, ws.data_ptr(), 4096)
     assert qd._workspace(0, None, CPU) == (None, None, 0)
     assert qd._workspace(4097, ws, CPU)[0] is not ws       # too small: a new one
+
+
+def test_attention_takes_no_longer_bound_than_the_table_holds(on_host):
+    """A slice of a wider table: its rows lie further apart than they are long,
+    and a bound beyond their length would look up pages past them."""
+    cache = qd.KV4Cache(4, 16, 2, 64, device="cpu")
+    q, lengths = torch.zeros((2, 4, 64), dtype=torch.float16), torch.zeros(2, dtype=torch.int32)
+    wide = torch.zeros((2, 50), dtype=torch.int32)
+    for table in (wide[:, :3], wide[:, 47:], wide[:, 3:6].contiguous()):
+        for bound in (49, 800):
+            with pytest.raises(ValueError, match="max_kv_len"):
+                qd.kv4_attention(q, cache, table, lengths, max_kv_len=bound)
+    with pytest.raises(ValueError, match="max_kv_len"):
+        qd.kv4_attention(q, cache, wide[:, :0], lengths, max_kv_len=1)

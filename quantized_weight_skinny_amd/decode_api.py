@@ -115,6 +115,8 @@ class KV4Cache:
     block holds exactly is 2688 times the scale, the finest step of a block's
     scale 2^-9 of it, so amax / 2688 of typical keys (values) is the choice."""
 
+    _FIXED = frozenset(("data", "device", "layers", "pages", "page_size", "kv_heads", "head_dim", "k_scale", "v_scale"))
+
     def __init__(self, pages, page_size, kv_heads, head_dim, layers=1, k_scale=1.0 / 128, v_scale=1.0 / 128,
                  device="cuda"):
         nbytes = qpn_kv4_page_bytes(page_size, kv_heads, head_dim)
@@ -136,19 +138,25 @@ class KV4Cache:
         return self
 
     def _init(self, data, page_size, kv_heads, head_dim, k_scale, v_scale):
-        self.data = data
+        k_scale, v_scale = (
+            [float(s)] * data.shape[0] if isinstance(s, (int, float)) else [float(x) for x in s]
+            for s in (k_scale, v_scale))
+        if len(k_scale) != data.shape[0] or len(v_scale) != data.shape[0]:
+            raise ValueError("k_scale and v_scale take one number, or one a layer")
+        if not all(math.isfinite(s) and s > 0 for s in k_scale + v_scale):
+            raise ValueError("tensor scales must be finite and above 0")
+        self.data, self.device = data, data.device
         self.layers, self.pages = data.shape[0], data.shape[1]
         self.page_size, self.kv_heads, self.head_dim = page_size, kv_heads, head_dim
-        self.k_scale, self.v_scale = (
-            [float(s)] * self.layers if isinstance(s, (int, float)) else [float(x) for x in s]
-            for s in (k_scale, v_scale))
-        if len(self.k_scale) != self.layers or len(self.v_scale) != self.layers:
-            raise ValueError("k_scale and v_scale take one number, or one a layer")
-        if not all(math.isfinite(s) and s > 0 for s in self.k_scale + self.v_scale):
-            raise ValueError("tensor scales must be finite and above 0")
-        self.k_scale, self.v_scale = tuple(self.k_scale), tuple(self.v_scale)  # the descriptors hold them
-        self.device = data.device
+        self.k_scale, self.v_scale = tuple(k_scale), tuple(v_scale)
         self._descs = [None] * self.layers
+
+    def __setattr__(self, name, value):
+        """The descriptors hold the buffer's address, its sizes and the scales, so
+        none of these is replaced: a new buffer is a new cache."""
+        if name in self._FIXED and name in self.__dict__:
+            raise AttributeError(f"a cache's {name} does not change: wrap the other buffer in a cache of its own")
+        super().__setattr__(name, value)
 
     def desc(self, layer=0):
         """The C descriptor with one layer's scales."""

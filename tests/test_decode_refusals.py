@@ -40,3 +40,19 @@ def test_attention_takes_no_longer_bound_than_the_table_holds(on_host):
                 qd.kv4_attention(q, cache, table, lengths, max_kv_len=bound)
     with pytest.raises(ValueError, match="max_kv_len"):
         qd.kv4_attention(q, cache, wide[:, :0], lengths, max_kv_len=1)
+
+
+def test_a_caches_fields_do_not_change():
+    """Its descriptors are built once a layer; a field replaced afterwards would
+    leave the calls at the old buffer (sizes, scales)."""
+    cache = qd.KV4Cache(4, 16, 2, 64, layers=2, device="cpu")
+    for name, value in (("data", cache.data.clone()), ("k_scale", (1.0, 1.0)), ("v_scale", (1.0, 1.0)), ("pages", 3),
+                        ("page_size", 32), ("kv_heads", 1), ("head_dim", 128), ("layers", 1),
+                        ("device", torch.device("cpu"))):
+        before = getattr(cache, name)
+        with pytest.raises(AttributeError, match=name):
+            setattr(cache, name, value)
+        assert getattr(cache, name) is before
+    cache.data[1, 2] = 7                                   # its bytes do
+    cache.label = "a user's own"
+    cache.label = "and again"

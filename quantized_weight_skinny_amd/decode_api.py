@@ -38,6 +38,13 @@ DTYPES = {torch.float16: QPN_DT_F16, torch.bfloat16: QPN_DT_BF16, torch.float32:
 HALVES = (torch.float16, torch.bfloat16)
 INT32_MAX = 2**31 - 1  # ctypes cuts a larger number to its low 32 bits without a word
 
+
+def _sizes(**sizes):
+    for name, x in sizes.items():
+        if not 0 <= x <= INT32_MAX:
+            raise ValueError(f"{name} must be 0 .. {INT32_MAX}, not {x}")
+
+
 # A verify step makes these calls once a layer, so what Python adds to each
 # counts: checks compare plain attributes, the descriptors of a cache are built
 # once, and the current stream is taken as the raw handle that torch keeps.
@@ -119,6 +126,7 @@ class KV4Cache:
 
     def __init__(self, pages, page_size, kv_heads, head_dim, layers=1, k_scale=1.0 / 128, v_scale=1.0 / 128,
                  device="cuda"):
+        _sizes(page_size=page_size, kv_heads=kv_heads, head_dim=head_dim)
         nbytes = qpn_kv4_page_bytes(page_size, kv_heads, head_dim)
         if nbytes == 0:
             raise ValueError(f"a page of {page_size} tokens, {kv_heads} heads of {head_dim} is not supported: 16, 32, "
@@ -130,6 +138,7 @@ class KV4Cache:
     def wrap(cls, data, page_size, kv_heads, head_dim, k_scale=1.0 / 128, v_scale=1.0 / 128):
         """A cache over an existing buffer, uint8 [layers, pages, page_bytes]."""
         self = cls.__new__(cls)
+        _sizes(page_size=page_size, kv_heads=kv_heads, head_dim=head_dim)
         _on_device(data, "data")
         nbytes = qpn_kv4_page_bytes(page_size, kv_heads, head_dim)
         if data.dtype != torch.uint8 or data.dim() != 3 or not data.is_contiguous() or data.shape[2] != nbytes or not nbytes:
@@ -225,6 +234,7 @@ def kv4_attention_workspace(cache, rows, heads, batch, max_q_len, max_kv_len):
     """A workspace for kv4_attention with these sizes (None when none is
     needed). It carries nothing from call to call, but two calls that may run
     at once need one each."""
+    _sizes(rows=rows, heads=heads, batch=batch, max_q_len=max_q_len, max_kv_len=max_kv_len)
     need = _attention_workspace_bytes(cache.page_size, cache.kv_heads, cache.head_dim, rows, heads, batch, max_q_len,
                                       max_kv_len)
     return torch.empty(need, dtype=torch.uint8, device=cache.device) if need else None
@@ -291,6 +301,7 @@ _verify_workspace_bytes = functools.lru_cache(maxsize=256)(qpn_verify_workspace_
 def verify_workspace(batch, drafts, vocab, device="cuda"):
     """A workspace for verify_drafts with these sizes. It carries nothing from
     call to call, but two calls that may run at once need one each."""
+    _sizes(batch=batch, drafts=drafts, vocab=vocab)
     need = _verify_workspace_bytes(batch, drafts, vocab)
     return torch.empty(need, dtype=torch.uint8, device=device) if need else None
 

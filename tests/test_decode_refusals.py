@@ -56,3 +56,24 @@ def test_a_caches_fields_do_not_change():
     cache.data[1, 2] = 7                                   # its bytes do
     cache.label = "a user's own"
     cache.label = "and again"
+
+
+FAR = 1 << 32   # a number that ctypes would cut to its low 32 bits
+
+
+def test_sizes_beyond_32_bits_are_refused(on_host):
+    for page_size, kv_heads, head_dim in ((FAR + 16, 2, 64), (16, FAR + 2, 64), (16, 2, FAR + 64), (16 - FAR, 2, 64)):
+        with pytest.raises(ValueError, match="must be 0"):
+            qd.KV4Cache(4, page_size, kv_heads, head_dim, device="cpu")
+        with pytest.raises(ValueError, match="must be 0"):
+            qd.KV4Cache.wrap(torch.zeros((1, 4, 16 * 2 * 72), dtype=torch.uint8), page_size, kv_heads, head_dim)
+    cache = qd.KV4Cache(4, 16, 2, 64, device="cpu")
+    sizes = dict(rows=8, heads=4, batch=2, max_q_len=4, max_kv_len=4096)
+    assert qd.kv4_attention_workspace(cache, **sizes).numel() > 0
+    for name in sizes:
+        with pytest.raises(ValueError, match=name):
+            qd.kv4_attention_workspace(cache, **dict(sizes, **{name: sizes[name] + FAR}))
+    assert qd.verify_workspace(2, 3, 100, device="cpu").numel() > 0
+    for sizes in ((FAR + 2, 3, 100), (2, FAR + 3, 100), (2, 3, FAR + 100), (2 - FAR, 3, 100)):
+        with pytest.raises(ValueError, match="must be 0"):
+            qd.verify_workspace(*sizes, device="cpu")

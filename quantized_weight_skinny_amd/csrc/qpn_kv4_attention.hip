@@ -20,9 +20,10 @@
 //    together by swapping nibbles, before they are decoded.
 //  - the result of O^T: row i, elements (4g + r) * D/16 + n: over n contiguous.
 //
-// E2M1 x E4M3 is exact in fp16, so fp16 rounds only q (bf16 rows are scaled
-// by a power of two first: exact but for elements 2^-24 below their row's
-// largest) and p. p is kept between 2^8 (at the reference) and 2^15: a row's
+// E2M1 x E4M3 is exact in fp16, so fp16 rounds only q (bf16 rows are scaled by
+// a power of two first, their largest to 2^15: all eight bits of an element
+// stay down to 2^-32 of its row's largest, and what a smaller one loses is at
+// most 2^-40 of that) and p. p is kept between 2^8 (at the reference) and 2^15: a row's
 // reference moves only when a score passes it by 2^7, which a wavefront sees
 // with one vote, and p as small as 2^-22 of the largest is a normal fp16.
 //
@@ -426,8 +427,9 @@ __global__ __launch_bounds__(kW * 64, attn_waves_per_simd(DIM, NQ)) void kv4_att
         }
         return x;
       };
-      // bf16: the exponent (clamped: a row below 2^-60 by 2^60; inf and NaN stay
-      // themselves) that brings a row's largest magnitude to [1, 2).
+      // bf16: the exponent (a row below 2^-111 takes that of 2^-111; inf and NaN stay
+      // themselves) less which a row's largest magnitude is in [2^15, 2^16): the
+      // top of fp16, whose smallest step is then 2^-39 of it.
       const auto larger = [](uint32_t top, const u4& x) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) top = max(max(top, x[e] & 0x7FFFu), (x[e] >> 16) & 0x7FFFu);
@@ -436,7 +438,7 @@ __global__ __launch_bounds__(kW * 64, attn_waves_per_simd(DIM, NQ)) void kv4_att
       const auto exponent = [](uint32_t top) {
         top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16)));
         top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32)));
-        return min(max(static_cast<int>(top >> 7), 67), 252) - 127;
+        return min(max(static_cast<int>(top >> 7), 16), 254) - (127 + 15);
       };
       const auto fragment = [&](int n, u4 x, int e2) {
         if (n * 16 + i >= nrows) x = u4{0u, 0u, 0u, 0u};

@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 
 @pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("group", [1, 5, 8])
-@pytest.mark.parametrize("strong", [2.0 ** 20, -2.0 ** 100])
+@pytest.mark.parametrize("strong", [2.0 ** 20, -2.0 ** 100, 2.0 ** -80])
 def test_bf16_rows_with_one_strong_channel_keep_the_others(dim, group, strong):
     """A query element far above its row's others, where every cached key is 0
     (a channel of a block that holds larger ones): the scores come from

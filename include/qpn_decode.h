@@ -55,7 +55,8 @@ size_t qpn_kv4_page_bytes(int32_t page_size, int32_t kv_heads, int32_t head_dim)
  * codes E2M1(x / (scale * tensor scale)), in fp32, nearest with ties to even:
  * the rule of qpn_quantize_nvfp4. +-inf is held as the largest value of its
  * block, NaN as 0 (the cache has no code for them). A slot outside the pool
- * is skipped; two equal slots in one call leave either token there. */
+ * is skipped. No slot may be given twice in one call: its blocks would be those
+ * of either token, codes of one under scales of the other among them. */
 qpn_status qpn_kv4_append(const qpn_kv4_cache* cache, int32_t layer, const void* k_dev, const void* v_dev,
                           int32_t dtype, int64_t tokens, int64_t k_token_stride, int64_t k_head_stride,
                           int64_t v_token_stride, int64_t v_head_stride, const int64_t* slots_dev, void* stream);
@@ -83,8 +84,13 @@ qpn_status qpn_kv4_copy_pages(const qpn_kv4_cache* cache, const int32_t* src_dev
  *   lse[row][head] = log sum_t exp(scale * q . k_t)            (fp32, may be NULL)
  * A row that sees no token (a length of 0, a position below 0) gets zeros and
  * -inf. A page index outside the pool holds no tokens: its positions are not
- * seen. Products of the exact cached values with q in fp16 (a bf16 row scaled
- * by a power of two first), all sums in fp32. */
+ * seen. Rows that no sequence has are not written. Cached values enter the
+ * products exactly, all sums are fp32, and two factors are rounded to fp16:
+ *  - q of bf16, scaled by a power of two that takes a row's largest element to
+ *    2^15: elements keep their 8 bits down to 2^-32 of it, smaller ones are off
+ *    by at most 2^-40 of it;
+ *  - the softmax weights before their product with v: each is off by at most
+ *    2^-11 of itself or 2^-33 of the row's largest. lse sums them unrounded. */
 typedef struct {
   const void* q;           /* device: [rows][heads][head_dim] by strides */
   void* out;               /* device: contiguous, 16-byte aligned */
@@ -132,7 +138,11 @@ qpn_status qpn_kv4_attention(const qpn_kv4_cache* cache, const qpn_kv4_attention
  * temperature 1. NaN logits count as -inf, NaN and negative probabilities as
  * 0. A draft token outside 0 .. vocab - 1 is not accepted. If nothing is left
  * over, the token is picked from p; if p is all zero, it is -1.
- * Probabilities (probabilities = 1): fp32 p and q are taken as they are. */
+ * Probabilities (probabilities = 1): fp32 p and q are taken as they are.
+ * From logits, the row sums behind the accept tests and logprobs add 32-bit
+ * exponentials in 64 bits: p and q are good to about 2^-21 of themselves, and a
+ * test closer to its border than that may go either way. The token is picked
+ * with 64-bit exponentials and sums. */
 typedef struct {
   const void* target;           /* device: [batch][drafts + 1][vocab] by strides */
   const void* draft;            /* device: [batch][drafts][vocab] by strides, same dtype, or NULL */

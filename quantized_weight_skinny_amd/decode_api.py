@@ -184,7 +184,7 @@ def kv4_append(cache, k, v, slots, layer=0):
     """Quantizes k and v ([tokens, kv_heads, head_dim] fp16 or bf16, any
     strides with a contiguous last dimension: slices of a fused projection's
     output will do) into the pages' slots (int64 [tokens], page * page_size +
-    offset; one outside the pool is skipped)."""
+    offset; one outside the pool is skipped, none may be given twice)."""
     dev = cache.device
     tokens = slots.shape[0]
     shape = (tokens, cache.kv_heads, cache.head_dim)
@@ -252,7 +252,9 @@ def kv4_attention(q, cache, table, kv_len, q_start=None, max_q_len=None, max_kv_
     can hold); a bound of 512 or less spares a small call its second launch.
     window > 0: a row sees the last `window` tokens up to its own. out [rows,
     heads, head_dim] like q, lse fp32 [rows, heads]; a row that sees no token
-    gets zeros and -inf."""
+    gets zeros and -inf. The softmax weights are rounded to fp16 before the
+    product with the values, and so are bf16 queries, scaled first (bounds in
+    qpn_decode.h); sums are fp32."""
     dev = cache.device
     dim, kv_heads = cache.head_dim, cache.kv_heads
     _on_device(q, "q", dev)
@@ -319,7 +321,9 @@ def verify_drafts(target, draft_tokens, u_accept, u_sample, draft=None, num_draf
     None: 1); u_accept fp32 [batch, drafts] and u_sample fp32 [batch]: random
     numbers in [0, 1). probabilities=True: target and draft are fp32
     probabilities instead, taken as they are. The accepted drafts come first,
-    then the token that replaces or follows them, then -1 (log-probability 0)."""
+    then the token that replaces or follows them, then -1 (log-probability 0).
+    Accept tests and log-probabilities of logits use p and q to about 2^-21 of
+    themselves, the pick of the token 64 bits."""
     _on_device(target, "target")
     dev = target.device
     if target.dim() != 3:

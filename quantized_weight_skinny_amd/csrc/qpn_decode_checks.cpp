@@ -22,7 +22,9 @@ constexpr int64_t kMaxGroups = int64_t(1) << 23;  // workgroups of a launch: 2^3
 // row of 5 heads a kv head; whole / cut): 8 runs of 512 tokens 7.3 / 9.3 us,
 // of 1024 10.5 / 9.4; 128 of 1024 12.7 / 15.6, of 2048 20.7 / 18.4; 512 of
 // 1024 17.8 / 31.3, of 4096 58 / 65. They meet near 512 tokens for 8 runs and
-// at twice that for four times the runs.
+// at twice that for four times the runs. (All of equal lengths at their bound. The
+// rule knows the bound alone: many runs of which one is long go whole too, and
+// that one then takes its workgroup as long as its tiles do.)
 bool whole_runs(int64_t tokens, int64_t runs) { return tokens <= 512 || tokens * tokens <= 32768 * runs; }
 
 bool positive(float x) { return isfinite(x) && x > 0.0f; }

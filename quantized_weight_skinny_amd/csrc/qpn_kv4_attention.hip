@@ -31,14 +31,15 @@
 // and 64 multiplications (the conversion's own scale is a power of two, the
 // blocks' are not) and 16 instructions to pair V's; every row tile adds 8
 // exponentials at two slots each, 24 adds and multiply-adds, 4 conversions, 6
-// for the maximum and 16 MFMAs. At three row tiles (8 rows of 5 heads) that
-// counts to 1600 cycles a SIMD; 1670 are measured, with two wavefronts, which
-// a SIMD needs: one alone issues a vector instruction every 8 cycles, two or
-// more every 4 to 5. So 131072 tokens of 8 heads (151 MB) take 27 us of vector
-// instructions against 25 us of memory, and the call 47: the rest is the
-// launch (2), the shares' counting and first loads (6), joining wavefronts (3)
-// and pieces (6), and what memory's latency leaves open. At one row tile (one
-// row, four wavefronts a SIMD) 24 sequences' 180 MB take 39 us.
+// for the maximum and 16 MFMAs. At three row tiles (8 rows of 5 heads) the
+// counters give 364 vector instructions a tile, all of the kernel's, that issue for
+// 1570 cycles; the loop takes 1810 cycles a tile and SIMD, with two wavefronts,
+// which a SIMD needs: one alone issues a vector instruction every 8 cycles, two
+// or more every 4 to 5. So 131072 tokens of 8 heads (151 MB) take 26 us of vector
+// instructions against 25 us of memory, and the call 46: the loop is 30 of it,
+// the rest the launch (1 to 2), the shares' counting (3), first loads (3), joining
+// wavefronts (4) and pieces (6). At one row tile (one row, four wavefronts a
+// SIMD) 24 sequences' 180 MB take 39 us.
 #include "qpn_device.hpp"
 #include "qpn_decode_internal.hpp"
 
@@ -461,8 +462,9 @@ __global__ __launch_bounds__(kW * 64, attn_waves_per_simd(DIM, NQ)) void kv4_att
       // They are asked for before the first keys and values and made into
       // fragments while those come; in LDS, wavefront n does tile n for all four.
       // Two tiles (of 128 at three wavefronts a SIMD, of 256) would have too many
-      // registers on the way: those queries come first, eight elements at a time,
-      // bf16 rows twice.
+      // registers on the way (made as the others the compiler spills 8 of 168 at
+      // 128 in bf16 and 16 of 256 at 256): those queries come first, eight elements
+      // at a time, bf16 rows twice, and the first keys wait for them.
       static_assert(NQ <= kW, "a wavefront prepares one tile");
       constexpr bool kQueriesFirst = NQ == 2 && DIM >= 128;
       u4 raw[kQueriesFirst ? 1 : kQueriesInLds ? 1 : NQ][kQueriesFirst ? 1 : kSteps];
@@ -613,8 +615,11 @@ __global__ __launch_bounds__(kW * 64, attn_waves_per_simd(DIM, NQ)) void kv4_att
       // behind goes first.
       const int quarter = (mine + 3) / 4;
       __builtin_amdgcn_s_setprio(3);
-      // (Where the registers hold two tiles, three row tiles of 128, the whole next
-      // tile is asked for before this one's scores: 57 -> 54 us over 131072 tokens.)
+      // (At three row tiles of 128, whose registers hold two tiles, the whole next
+      // tile is asked for before this one's scores: 57 -> 54 us over 131072 tokens.
+      // Two tiles would spill at two and three row tiles of 64, one and two of 128 and
+      // two of 256; they would fit at one and four of 64 and one of 256, which were
+      // not measured.)
       constexpr bool kTwo = NQ * DIM == 384;
       auto step = [&](Tile<DIM>& t, Tile<DIM>& u, int j) {
         if (j == quarter) __builtin_amdgcn_s_setprio(2);

@@ -21,8 +21,8 @@
 // last pass, when that took 16.8).
 //
 // Measured, fp16, 151936 tokens. 1 sequence of 7 drafts without rows: first
-// pass 5.9 us, sums 7.8, last pass 7.0; 32 such sequences with draft logits:
-// 32.8 (146 MB, 4.5 TB/s), accept tests 5.2, sums 18.9, rest 16.4, last 11.1.
+// pass 4.8 us, sums 7.4, last pass 6.9; 32 such sequences with draft logits:
+// 31.5 (146 MB, 4.6 TB/s), accept tests 5.2, sums 18.7, rest 16.8, last 10.9.
 #include "qpn_decode_internal.hpp"
 #include "qpn_device.hpp"
 

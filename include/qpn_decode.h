@@ -90,7 +90,9 @@ qpn_status qpn_kv4_copy_pages(const qpn_kv4_cache* cache, const int32_t* src_dev
  *    2^15: elements keep their 8 bits down to 2^-32 of it, smaller ones are off
  *    by at most 2^-40 of it;
  *  - the softmax weights before their product with v: each is off by at most
- *    2^-11 of itself or 2^-33 of the row's largest. lse sums them unrounded. */
+ *    2^-11 of itself or 2^-33 of the row's largest. lse sums them unrounded.
+ * Scores (scale * q . k) are to be below 2^26 in magnitude, which fp32 holds to a
+ * few units: beyond 2^27 a row may come out as NaN, zeros or -inf. */
 typedef struct {
   const void* q;           /* device: [rows][heads][head_dim] by strides */
   void* out;               /* device: contiguous, 16-byte aligned */

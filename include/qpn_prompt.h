@@ -1,0 +1,79 @@
+/*
+ * qpn_prompt.h - C ABI of libqpn.so for a prompt's step, where qpn.h and
+ * qpn_decode.h serve steps of up to 16 rows: products of any number of rows
+ * with weights of 8 bits and a scale for each block of 128, attention of a
+ * chunk of new tokens over the 4-bit paged cache, and the log-probabilities of
+ * given tokens.
+ *
+ * The conventions of qpn.h hold: device pointers, caller-owned buffers, work
+ * enqueued on `stream` (NULL = the default stream) without waiting, arguments
+ * checked on the host before any HIP call, no memory allocated here, no
+ * global state. Every call may be captured into a HIP graph; lengths, tables
+ * and tokens are read on the device, so a replay follows their contents. A
+ * workspace's contents need no preparation and carry nothing to the next
+ * call; calls that may run at once need one each.
+ */
+#ifndef QPN_PROMPT_H
+#define QPN_PROMPT_H
+
+#include "qpn_decode.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* The type of x in a block product that is E4M3 codes already. */
+#define QPN_DT_E4M3 4
+
+/* Quantizes x [rows][k] of `dtype` (F16, BF16 or F32, rows `stride` elements
+ * apart) to E4M3 codes with a scale for each 128 columns and `block_rows` rows
+ * (1: activations; 128: weights): the least power of two s >= 2^-126 with
+ * amax <= 448 s, 1 for a block of zeros. code = E4M3(x / s), nearest with ties
+ * to even; the quotient is exact, so each code is the nearest there is. inf
+ * and NaN get the NaN code and do not count for amax. k may be any number; the
+ * last block of a row (and of the rows) may be short.
+ *   codes   [rows][k], rows code_stride bytes apart
+ *   scales  [ceil(rows / block_rows)][ceil(k / 128)] by strides in elements */
+qpn_status qpn_fp8_block_quantize(const void* x_dev, int32_t dtype, int64_t rows, int64_t k, int64_t stride,
+                                  int32_t block_rows, uint8_t* codes_dev, int64_t code_stride, float* scales_dev,
+                                  int64_t scale_row_stride, int64_t scale_block_stride, void* stream);
+
+/* y[m][n] = sum over k of (x code * x scale)[m][k] * (w code * w scale)[n][k],
+ * x with a scale for each row and 128 columns, w with one for each 128 rows
+ * and 128 columns (any fp32 scales). Products of codes are exact; the sum of a
+ * block and the scaled sums of the blocks are fp32; y is rounded once. With x
+ * of F16, BF16 or F32 it is quantized first, as by qpn_fp8_block_quantize with
+ * block_rows 1, into the workspace. NaN codes make the outputs that they enter
+ * NaN. */
+typedef struct {
+  const void* x;          /* device: [m][k] of x_dtype, rows x_stride elements apart */
+  const float* x_scales;  /* device: E4M3 x: [m][ceil(k / 128)] by strides; else NULL */
+  const uint8_t* w;       /* device: [n][k] E4M3 codes, 16-byte aligned */
+  const float* w_scales;  /* device: [ceil(n / 128)][ceil(k / 128)] by strides */
+  void* y;                /* device: [m][n] of y_dtype, rows y_stride elements apart */
+  int64_t x_stride;       /* E4M3 x: a multiple of 16, and x 16-byte aligned */
+  int64_t x_scale_row_stride;
+  int64_t x_scale_block_stride;
+  int64_t w_stride;       /* bytes, a multiple of 16 */
+  int64_t w_scale_row_stride;
+  int64_t w_scale_block_stride;
+  int64_t y_stride;       /* >= n */
+  int64_t m;              /* 0 .. 2^22 */
+  int64_t n;              /* 0 .. 2^24 */
+  int64_t k;              /* 0 .. 2^20, a multiple of 16 */
+  int32_t x_dtype;        /* F16, BF16, F32 or E4M3 */
+  int32_t y_dtype;        /* F16, BF16 or F32 */
+} qpn_fp8_block_gemm_args;
+
+/* Workspace of a call with these sizes, whatever the type of x (0 for sizes
+ * that are refused, and where none is needed). */
+size_t qpn_fp8_block_workspace_bytes(int64_t m, int64_t n, int64_t k);
+
+qpn_status qpn_fp8_block_gemm(const qpn_fp8_block_gemm_args* args, void* workspace_dev, size_t workspace_bytes,
+                              void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* QPN_PROMPT_H */

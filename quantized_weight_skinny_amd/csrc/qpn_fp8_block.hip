@@ -1,0 +1,535 @@
+// Products of 8-bit codes with a scale for each block of 128
+// (include/qpn_prompt.h): the quantizer, the product of a few rows and the
+// product of many.
+//
+// Mathematics. v_mfma_f32_16x16x128_f8f6f4 takes 128 places of k at once, one
+// block of either operand's scales: started from zero it gives the block's
+// sums, and one multiply-add each adds them, times (x scale * w scale), to the
+// fp32 result. w is the A operand (16 outputs), x the B operand (16 rows), so a
+// lane's results are one row of x at four neighbouring outputs: one factor for
+// all four, and stores of four. Lane l = (i, g) = (l % 16, l / 16) holds row i;
+// which 32 of the 128 places it holds is free as long as both operands agree:
+// the 16-byte pieces g and g + 4.
+//
+// What the instruction keeps of a sum. It adds the products of codes with some
+// 12 bits below the largest of them, not 24: blocks of normal values come out
+// 1.4e-5 of the result off (the 2-norms), measured, and the same for
+// v_mfma_f32_16x16x32_fp8_fp8. That is a tenth and less of the rounding to
+// fp16 or bf16, and too much for an fp32 result: there the codes are brought
+// to fp16, which holds them exactly, for v_mfma_f32_16x16x32_f16, whose sums are
+// fp32 (EXACT below), at half the rate.
+#include "qpn_decode_internal.hpp"
+#include "qpn_device.hpp"
+#include "qpn_prompt_internal.hpp"
+
+namespace qpn {
+namespace {
+
+typedef int i8 __attribute__((ext_vector_type(8)));
+typedef u4 u4_anywhere __attribute__((aligned(2)));
+
+// ------------------------------------------------------------------ quantizer
+
+// 8 elements of type DT from element `at` of a row; those from `end` on are 0.
+template <int DT>
+__device__ __forceinline__ void load8(const void* row, int64_t at, int64_t end, bool vec, float (&v)[8]) {
+  if constexpr (DT == QPN_DT_F32) {
+    const float* p = static_cast<const float*>(row) + at;
+    if (vec && at + 8 <= end) {
+      const f4 a = *reinterpret_cast<const f4*>(p), b = *reinterpret_cast<const f4*>(p + 4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = a[e], v[4 + e] = b[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = at + e < end ? p[e] : 0.f;
+    }
+  } else {
+    constexpr bool kBf16 = DT == QPN_DT_BF16;
+    const uint16_t* p = static_cast<const uint16_t*>(row) + at;
+    if (vec && at + 8 <= end) {
+      const u4 x = *reinterpret_cast<const u4*>(p);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[2 * e] = widen16<kBf16>(x[e] & 0xFFFFu), v[2 * e + 1] = widen16<kBf16>(x[e] >> 16);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = at + e < end ? widen16<kBf16>(p[e]) : 0.f;
+    }
+  }
+}
+
+// The magnitude as it counts for a block's scale: 0 for inf and NaN.
+__device__ __forceinline__ float counted(float x) {
+  const float a = fabsf(x);
+  return a < __builtin_inff() ? a : 0.f;
+}
+
+// The exponent e of the scale 2^e: amax = f 2^q with 1 <= f < 2, and 448 = 1.75 * 2^8.
+__device__ __forceinline__ int scale_exponent(float amax) {
+  if (amax == 0.f) return 0;
+  const uint32_t b = __float_as_uint(amax);
+  const int q = static_cast<int>(b >> 23) - 127;  // (a subnormal amax gets the least scale)
+  return max(q - 8 + ((b & 0x7FFFFFu) > 0x600000u), -126);
+}
+
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// Codes of 8 elements: exact quotients (a multiplication by a power of two),
+// rounded to nearest even by the conversion; nothing is above 448.
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {
+  float q[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) q[e] = fabsf(v[e]) < __builtin_inff() ? v[e] * inv : __builtin_nanf("");
+  uint2 r;
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+  r.x = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w, true);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], 0, false);
+  r.y = __builtin_amdgcn_cvt_pk_fp8_f32(q[6], q[7], w, true);
+  return r;
+}
+
+__device__ __forceinline__ void store_codes8(uint8_t* row, int64_t at, int64_t end, bool vec, uint2 c) {
+  if (vec && at + 8 <= end) {
+    *reinterpret_cast<uint2*>(row + at) = c;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (at + e < end) row[at + e] = static_cast<uint8_t>((e < 4 ? c.x : c.y) >> (8 * (e & 3)));
+  }
+}
+
+struct QuantizeParams {
+  const void* x;
+  uint8_t* codes;
+  float* scales;
+  int64_t rows, k, stride, code_stride, scale_row_stride, scale_block_stride;
+  int32_t blocks, load_vec, store_vec;
+};
+
+// A row's block of 128 is 16 lanes'.
+template <int DT>
+__global__ __launch_bounds__(256) void quantize_rows_kernel(const QuantizeParams a) {
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 16 + threadIdx.x / 16;
+  const int64_t row = t / a.blocks;
+  if (row >= a.rows) return;
+  const int block = static_cast<int>(t - row * a.blocks);
+  const int64_t at = static_cast<int64_t>(block) * kScaleBlock + threadIdx.x % 16 * 8;
+  const int size = DT == QPN_DT_F32 ? 4 : 2;
+  float v[8];
+  load8<DT>(static_cast<const char*>(a.x) + row * a.stride * size, at, a.k, a.load_vec, v);
+  float amax = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) amax = fmaxf(amax, counted(v[e]));
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
+  const int e2 = scale_exponent(amax);
+  store_codes8(a.codes + row * a.code_stride, at, a.k, a.store_vec, codes8(v, pow2(-e2)));
+  if (threadIdx.x % 16 == 0) a.scales[row * a.scale_row_stride + block * a.scale_block_stride] = pow2(e2);
+}
+
+// 128 x 128 elements are one workgroup's.
+template <int DT>
+__global__ __launch_bounds__(256) void quantize_blocks_kernel(const QuantizeParams a) {
+  __shared__ float top[4];
+  const int64_t rb = blockIdx.x / a.blocks;
+  const int block = static_cast<int>(blockIdx.x - rb * a.blocks);
+  const int64_t at = static_cast<int64_t>(block) * kScaleBlock + threadIdx.x % 16 * 8;
+  const int size = DT == QPN_DT_F32 ? 4 : 2;
+  float amax = 0.f;
+  float v[8][8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int64_t row = rb * kScaleBlock + j * 16 + threadIdx.x / 16;
+    load8<DT>(static_cast<const char*>(a.x) + min(row, a.rows - 1) * a.stride * size, at, a.k, a.load_vec, v[j]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, counted(v[j][e]));  // (the last row again changes nothing)
+  }
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
+  if (threadIdx.x % 64 == 0) top[threadIdx.x / 64] = amax;
+  __syncthreads();
+  const int e2 = scale_exponent(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int64_t row = rb * kScaleBlock + j * 16 + threadIdx.x / 16;
+    if (row < a.rows) store_codes8(a.codes + row * a.code_stride, at, a.k, a.store_vec, codes8(v[j], pow2(-e2)));
+  }
+  if (threadIdx.x == 0) a.scales[rb * a.scale_row_stride + block * a.scale_block_stride] = pow2(e2);
+}
+
+// ------------------------------------------------------------------ products
+
+struct ProductParams {
+  const uint8_t *x, *w;
+  const float *xs, *ws;
+  void* y;
+  float* partial;  // [splits][m][n] where splits > 1
+  int64_t x_stride, xs_row, xs_block, w_stride, ws_row, ws_block, y_stride;
+  int64_t m, n;
+  int32_t k, blocks, splits, y_dtype, y_vec;
+};
+
+// 32 codes of one row: a lane's part of a block, as fp16 where EXACT.
+template <bool EXACT>
+struct Frag {
+  u4 c[2];
+  __device__ __forceinline__ Frag() = default;
+  __device__ __forceinline__ Frag(const u4& c0, const u4& c1) : c{c0, c1} {}
+};
+template <>
+struct Frag<true> {
+  h8 c[4];
+  __device__ __forceinline__ Frag() = default;
+  __device__ __forceinline__ Frag(const u4& c0, const u4& c1)
+      : c{decode_fp8x8(c0[0], c0[1]), decode_fp8x8(c0[2], c0[3]), decode_fp8x8(c1[0], c1[1]), decode_fp8x8(c1[2], c1[3])} {}
+};
+
+// The block's sums.
+__device__ __forceinline__ f4 block_sums(const Frag<true>& w, const Frag<true>& x) {
+  f4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) s = __builtin_amdgcn_mfma_f32_16x16x32_f16(w.c[j], x.c[j], s, 0, 0, 0);
+  return s;
+}
+__device__ __forceinline__ f4 block_sums(const Frag<false>& w, const Frag<false>& x) {
+  const u4 &a0 = w.c[0], &a1 = w.c[1], &b0 = x.c[0], &b1 = x.c[1];
+  const i8 a = {(int)a0[0], (int)a0[1], (int)a0[2], (int)a0[3], (int)a1[0], (int)a1[1], (int)a1[2], (int)a1[3]};
+  const i8 b = {(int)b0[0], (int)b0[1], (int)b0[2], (int)b0[3], (int)b1[0], (int)b1[1], (int)b1[2], (int)b1[3]};
+  // both operands E4M3, no scales of the instruction's own
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+}
+
+// Four neighbouring outputs of one row.
+__device__ __forceinline__ void store4(const ProductParams& p, int64_t row, int64_t n, const f4& v) {
+  if (row >= p.m) return;
+  const int64_t at = row * p.y_stride + n;
+  if (p.y_dtype == QPN_DT_F32) {
+    float* y = static_cast<float*>(p.y) + at;
+    if (p.y_vec && n + 4 <= p.n) {
+      *reinterpret_cast<f4*>(y) = v;
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (n + r < p.n) y[r] = v[r];
+    }
+    return;
+  }
+  uint16_t h[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) h[r] = p.y_dtype == QPN_DT_BF16 ? round16<true>(v[r]) : round16<false>(v[r]);
+  uint16_t* y = static_cast<uint16_t*>(p.y) + at;
+  if (p.y_vec && n + 4 <= p.n) {
+    *reinterpret_cast<uint2*>(y) = uint2{h[0] | static_cast<uint32_t>(h[1]) << 16, h[2] | static_cast<uint32_t>(h[3]) << 16};
+  } else {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (n + r < p.n) y[r] = h[r];
+  }
+}
+
+// Few rows: a workgroup takes 16 outputs, its wavefronts every WAVES-th block
+// of k each, straight from memory into registers; their sums are added in LDS
+// in the order of the wavefronts.
+template <int MT, int WAVES, bool EXACT>
+__global__ __launch_bounds__(WAVES * 64) void few_rows_kernel(const ProductParams p) {
+  __shared__ f4 red[WAVES][MT][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+  const int i = lane & 15, g = lane >> 4;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
+  const uint8_t* w = p.w + n0 * p.w_stride;
+  const int w_row = static_cast<int>(min(static_cast<int64_t>(i), p.n - 1 - n0) * p.w_stride) + g * 16;
+  const float* ws = p.ws + n0 / kScaleBlock * p.ws_row;
+  int64_t x_row[MT];
+  const float* xs[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const int64_t row = min(static_cast<int64_t>(t * 16 + i), p.m - 1);
+    x_row[t] = row * p.x_stride + g * 16;
+    xs[t] = p.xs + row * p.xs_row;
+  }
+  f4 acc[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) acc[t] = f4{0.f, 0.f, 0.f, 0.f};
+  constexpr int kDepth = MT == 1 ? 4 : 2;
+  const u4 zero = {0u, 0u, 0u, 0u};
+#pragma unroll 1
+  for (int b0 = wave; b0 < p.blocks; b0 += WAVES * kDepth) {
+    u4 wa[kDepth][2], xa[kDepth][MT][2];
+    float s[kDepth][MT];
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+      const int b = b0 + d * WAVES, at = b * kScaleBlock;
+      // (a piece past the end of k, and a block past the last, is zeros)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bool in = at + g * 16 + h * 64 < p.k;
+        wa[d][h] = in ? __builtin_nontemporal_load(reinterpret_cast<const u4*>(w + w_row + at + h * 64)) : zero;
+#pragma unroll
+        for (int t = 0; t < MT; ++t) xa[d][t][h] = in ? *reinterpret_cast<const u4*>(p.x + x_row[t] + at + h * 64) : zero;
+      }
+      const int bb = min(b, p.blocks - 1);
+      const float sw = ws[bb * p.ws_block];
+#pragma unroll
+      for (int t = 0; t < MT; ++t) s[d][t] = b < p.blocks ? xs[t][bb * p.xs_block] * sw : 0.f;
+    }
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+      if (b0 + d * WAVES >= p.blocks) break;
+      const Frag<EXACT> wf(wa[d][0], wa[d][1]);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) acc[t] += block_sums(wf, Frag<EXACT>(xa[d][t][0], xa[d][t][1])) * s[d][t];
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < MT; ++t) red[wave][t][lane] = acc[t];
+  __syncthreads();
+  for (int t = wave; t < MT; t += WAVES) {
+    f4 v = red[0][t][lane];
+#pragma unroll
+    for (int o = 1; o < WAVES; ++o) v += red[o][t][lane];
+    store4(p, t * 16 + i, n0 + 4 * g, v);
+  }
+}
+
+// 64 lanes x 16 bytes from memory to LDS, past the registers: lane l's go to
+// dst + 16 l. M0 holds the place in LDS; the compiler does not track it, and
+// nothing else here uses it.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+typedef __attribute__((address_space(3))) void* lds_void;
+__device__ __forceinline__ void lds_dma(const uint8_t* base, uint32_t offset, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %2" ::"v"(offset), "s"(dst), "s"(base)
+               : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// Many rows: MW x NW wavefronts of TM x TN tiles of 16 x 16 each. Both
+// operands' 128 bytes of a block go to LDS, the next block's while this one is
+// multiplied. A row's eight 16-byte pieces lie in LDS at piece ^ (row % 8), so
+// that neighbouring rows' reads meet different banks.
+template <int MW, int NW, int TM, int TN, bool EXACT>
+__global__ __launch_bounds__(MW * NW * 64, 2) void many_rows_kernel(const ProductParams p) {
+  constexpr int kThreads = MW * NW * 64, kM = MW * TM * 16, kN = NW * TN * 16;
+  constexpr int kStage = (kM + kN) * kScaleBlock, kLoads = kStage / 16 / kThreads;
+  static_assert(kStage % (16 * kThreads) == 0 && kM * 8 % kThreads == 0, "whole loads of either operand");
+  static_assert(kScaleBlock % (TN * 16) == 0, "a wavefront's outputs share their scale");
+  __shared__ uint8_t lds[2][kStage];  // x rows, then w rows
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int i = lane & 15, g = lane >> 4;
+  const int64_t m_tiles = (p.m + kM - 1) / kM;
+  const int64_t m0 = blockIdx.x % m_tiles * kM, n0 = blockIdx.x / m_tiles * kN;
+  const int wm = wave % MW, wn = wave / MW;
+  const int split = blockIdx.y;
+  const int b0 = static_cast<int>(static_cast<int64_t>(p.blocks) * split / p.splits);
+  const int b1 = static_cast<int>(static_cast<int64_t>(p.blocks) * (split + 1) / p.splits);
+  const uint8_t* x = p.x + m0 * p.x_stride;
+  const uint8_t* w = p.w + n0 * p.w_stride;
+  // the rows and pieces that this thread brings: piece `tid` of every kThreads
+  uint32_t from[kLoads];
+#pragma unroll
+  for (int j = 0; j < kLoads; ++j) {
+    const int piece = j * kThreads + tid, row = piece / 8, c = (piece & 7) ^ (row & 7);
+    const bool of_x = j * kThreads < kM * 8;
+    const int64_t last = (of_x ? p.m - 1 - m0 : p.n - 1 - n0), r = of_x ? row : row - kM;
+    from[j] = static_cast<uint32_t>((r < last ? r : last) * (of_x ? p.x_stride : p.w_stride)) + c * 16;
+  }
+  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_void)(&lds[0][0])));
+  const auto load = [&](int b, int buf) {
+    const int at = b * kScaleBlock;
+    if (at + kScaleBlock <= p.k) {
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j)
+        lds_dma((j * kThreads < kM * 8 ? x : w) + at, from[j],
+                __builtin_amdgcn_readfirstlane(lds0 + buf * kStage + j * kThreads * 16 + wave * 1024));
+    } else {
+      // the short last block: pieces past the end of k are zeros
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) {
+        const int piece = j * kThreads + tid, c = (piece & 7) ^ (piece / 8 & 7);
+        u4 v = {0u, 0u, 0u, 0u};
+        if (at + c * 16 < p.k) v = *reinterpret_cast<const u4*>((j * kThreads < kM * 8 ? x : w) + at + from[j]);
+        *reinterpret_cast<u4*>(&lds[buf][piece * 16]) = v;
+      }
+    }
+  };
+  const float* ws = p.ws + (n0 + wn * TN * 16 < p.n ? (n0 + wn * TN * 16) / kScaleBlock : 0) * p.ws_row;
+  const float* xs = p.xs + m0 * p.xs_row;
+  uint32_t xs_row[TM];
+#pragma unroll
+  for (int t = 0; t < TM; ++t)
+    xs_row[t] = static_cast<uint32_t>(min(static_cast<int64_t>((wm * TM + t) * 16 + i), p.m - 1 - m0) * p.xs_row);
+  float sw, sx[TM];
+  const auto load_scales = [&](int b) {
+    sw = ws[b * p.ws_block];
+#pragma unroll
+    for (int t = 0; t < TM; ++t) sx[t] = (xs + b * p.xs_block)[xs_row[t]];
+  };
+  f4 acc[TM][TN];
+#pragma unroll
+  for (int t = 0; t < TM; ++t)
+#pragma unroll
+    for (int u = 0; u < TN; ++u) acc[t][u] = f4{0.f, 0.f, 0.f, 0.f};
+  const int slot0 = ((g ^ (i & 7)) * 16), slot1 = (((g + 4) ^ (i & 7)) * 16);
+  if (b0 < b1) {
+    load(b0, 0);
+    load_scales(b0);
+  }
+  for (int b = b0; b < b1; ++b) {
+    const int buf = (b - b0) & 1;
+    float s[TM];
+    __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < TM; ++t) s[t] = sx[t] * sw;
+    if (b + 1 < b1) {
+      load(b + 1, buf ^ 1);
+      load_scales(b + 1);
+    }
+    const uint8_t* xt = &lds[buf][(wm * TM * 16 + i) * kScaleBlock];
+    const uint8_t* wt = &lds[buf][(kM + wn * TN * 16 + i) * kScaleBlock];
+    const auto frag = [&](const uint8_t* rows) {
+      return Frag<EXACT>(*reinterpret_cast<const u4*>(rows + slot0), *reinterpret_cast<const u4*>(rows + slot1));
+    };
+    Frag<EXACT> wf[TN];
+#pragma unroll
+    for (int u = 0; u < TN; ++u) wf[u] = frag(wt + u * 16 * kScaleBlock);
+#pragma unroll
+    for (int t = 0; t < TM; ++t) {
+      const Frag<EXACT> xf = frag(xt + t * 16 * kScaleBlock);
+#pragma unroll
+      for (int u = 0; u < TN; ++u) acc[t][u] += block_sums(wf[u], xf) * s[t];
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < TM; ++t) {
+    const int64_t row = m0 + (wm * TM + t) * 16 + i;
+#pragma unroll
+    for (int u = 0; u < TN; ++u) {
+      const int64_t n = n0 + (wn * TN + u) * 16 + 4 * g;
+      if (p.splits == 1) {
+        store4(p, row, n, acc[t][u]);
+      } else if (row < p.m) {
+        float* d = p.partial + (split * p.m + row) * p.n + n;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (n + r < p.n) d[r] = acc[t][u][r];
+      }
+    }
+  }
+}
+
+// Adds the partial sums of a split k, in the order of k.
+__global__ __launch_bounds__(256) void join_kernel(const ProductParams p) {
+  const int64_t quads = (p.n + 3) / 4;
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t row = at / quads, n = (at - row * quads) * 4;
+  if (row >= p.m) return;
+  f4 v = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < p.splits; ++s) {
+    const float* d = p.partial + (s * p.m + row) * p.n + n;
+    if (p.n % 4 == 0) {
+      v += *reinterpret_cast<const f4*>(d);
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (n + r < p.n) v[r] += d[r];
+    }
+  }
+  store4(p, row, n, v);
+}
+
+template <int MT, bool EXACT>
+hipError_t launch_few(int waves, uint32_t grid, const ProductParams& p, hipStream_t stream) {
+  switch (waves) {
+    case 4: few_rows_kernel<MT, 4, EXACT><<<dim3(grid), dim3(256), 0, stream>>>(p); break;
+    case 8: few_rows_kernel<MT, 8, EXACT><<<dim3(grid), dim3(512), 0, stream>>>(p); break;
+    default:
+      if constexpr (MT == 4) return hipErrorInvalidValue;  // too many registers for 16 wavefronts
+      else few_rows_kernel<MT, 16, EXACT><<<dim3(grid), dim3(1024), 0, stream>>>(p);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_fp8_block_quantize(const void* x, int32_t dtype, int64_t rows, int64_t k, int64_t stride,
+                                     int32_t block_rows, uint8_t* codes, int64_t code_stride, float* scales,
+                                     int64_t scale_row_stride, int64_t scale_block_stride, hipStream_t stream) {
+  QuantizeParams a;
+  a.x = x, a.codes = codes, a.scales = scales;
+  a.rows = rows, a.k = k, a.stride = stride, a.code_stride = code_stride;
+  a.scale_row_stride = scale_row_stride, a.scale_block_stride = scale_block_stride;
+  a.blocks = static_cast<int32_t>((k + kScaleBlock - 1) / kScaleBlock);
+  const int per16 = dtype == QPN_DT_F32 ? 4 : 8;
+  a.load_vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && (stride % per16 == 0 || rows == 1);
+  a.store_vec = reinterpret_cast<uintptr_t>(codes) % 8 == 0 && (code_stride % 8 == 0 || rows == 1);
+  if (block_rows == 1) {
+    const dim3 grid(static_cast<uint32_t>((rows * a.blocks + 15) / 16));
+    switch (dtype) {
+      case QPN_DT_F16: quantize_rows_kernel<QPN_DT_F16><<<grid, dim3(256), 0, stream>>>(a); break;
+      case QPN_DT_BF16: quantize_rows_kernel<QPN_DT_BF16><<<grid, dim3(256), 0, stream>>>(a); break;
+      default: quantize_rows_kernel<QPN_DT_F32><<<grid, dim3(256), 0, stream>>>(a); break;
+    }
+  } else {
+    const dim3 grid(static_cast<uint32_t>((rows + kScaleBlock - 1) / kScaleBlock * a.blocks));
+    switch (dtype) {
+      case QPN_DT_F16: quantize_blocks_kernel<QPN_DT_F16><<<grid, dim3(256), 0, stream>>>(a); break;
+      case QPN_DT_BF16: quantize_blocks_kernel<QPN_DT_BF16><<<grid, dim3(256), 0, stream>>>(a); break;
+      default: quantize_blocks_kernel<QPN_DT_F32><<<grid, dim3(256), 0, stream>>>(a); break;
+    }
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_fp8_block_gemm(const qpn_fp8_block_gemm_args& a, const Fp8BlockPlan& plan, void* workspace,
+                                 hipStream_t stream) {
+  ProductParams p;
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  float* own_scales = reinterpret_cast<float*>(base + plan.code_bytes);
+  if (a.x_dtype == QPN_DT_E4M3) {
+    p.x = static_cast<const uint8_t*>(a.x), p.x_stride = a.x_stride;
+    p.xs = a.x_scales, p.xs_row = a.x_scale_row_stride, p.xs_block = a.x_scale_block_stride;
+  } else {
+    p.x = base, p.x_stride = a.k;
+    p.xs = own_scales, p.xs_row = 1, p.xs_block = a.m;  // a block's scales of neighbouring rows lie together
+    if (a.k > 0) {
+      const hipError_t e = launch_fp8_block_quantize(a.x, a.x_dtype, a.m, a.k, a.x_stride, 1, base, a.k, own_scales, 1,
+                                                     a.m, stream);
+      if (e != hipSuccess) return e;
+    }
+  }
+  p.w = a.w, p.w_stride = a.w_stride;
+  p.ws = a.w_scales, p.ws_row = a.w_scale_row_stride, p.ws_block = a.w_scale_block_stride;
+  p.y = a.y, p.y_stride = a.y_stride, p.y_dtype = a.y_dtype;
+  const int size = a.y_dtype == QPN_DT_F32 ? 4 : 2;
+  p.y_vec = reinterpret_cast<uintptr_t>(a.y) % (4 * size) == 0 && (a.y_stride % 4 == 0 || a.m == 1);
+  p.m = a.m, p.n = a.n, p.k = static_cast<int32_t>(a.k), p.blocks = plan.blocks, p.splits = plan.splits;
+  p.partial = reinterpret_cast<float*>(base + plan.code_bytes + plan.scale_bytes);
+  if (plan.m_tiles > 0) {
+    const uint32_t grid = static_cast<uint32_t>((a.n + 15) / 16);
+    const bool exact = a.y_dtype == QPN_DT_F32;
+    switch (plan.m_tiles) {
+      case 1: return exact ? launch_few<1, true>(plan.waves, grid, p, stream) : launch_few<1, false>(plan.waves, grid, p, stream);
+      case 2: return exact ? launch_few<2, true>(plan.waves, grid, p, stream) : launch_few<2, false>(plan.waves, grid, p, stream);
+      case 3: return exact ? launch_few<3, true>(plan.waves, grid, p, stream) : launch_few<3, false>(plan.waves, grid, p, stream);
+      default: return exact ? launch_few<4, true>(plan.waves, grid, p, stream) : launch_few<4, false>(plan.waves, grid, p, stream);
+    }
+  }
+  // (two times 4 fp16 fragments and their 32 results beside 128 sums would not fit the registers)
+  const bool exact = a.y_dtype == QPN_DT_F32;
+  const int tile = exact ? 128 : plan.tile;
+  const int64_t tiles = (a.m + tile - 1) / tile * ((a.n + tile - 1) / tile);
+  const dim3 grid(static_cast<uint32_t>(tiles), static_cast<uint32_t>(plan.splits));
+  if (exact)
+    many_rows_kernel<2, 2, 4, 4, true><<<grid, dim3(256), 0, stream>>>(p);
+  else if (tile == 256)
+    many_rows_kernel<2, 4, 8, 4, false><<<grid, dim3(512), 0, stream>>>(p);
+  else
+    many_rows_kernel<2, 2, 4, 4, false><<<grid, dim3(256), 0, stream>>>(p);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || plan.splits == 1) return e;
+  const int64_t quads = a.m * ((a.n + 3) / 4);
+  join_kernel<<<dim3(static_cast<uint32_t>((quads + 255) / 256)), dim3(256), 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+}  // namespace qpn

@@ -1,0 +1,30 @@
+// Host-side argument checks and sizes of include/qpn_prompt.h, in plain C++
+// (no HIP), so that they run under sanitizers without a GPU.
+#pragma once
+
+#include "../../include/qpn_prompt.h"
+#include "qpn_decode_checks.hpp"
+
+namespace qpn {
+
+constexpr int kScaleBlock = 128;  // elements along k (and rows of a weight) under one scale
+
+// The shape of a block product, chosen by plan_fp8_block.
+struct Fp8BlockPlan {
+  int m_tiles;       // > 0: a wavefront takes all rows, this many tiles of 16; 0: tiles in LDS
+  int waves;         // wavefronts of a workgroup that share k (m_tiles > 0)
+  int tile;          // 128 or 256: rows and columns of an LDS tile
+  int splits;        // k ranges, each to partial sums of its own; 1: none
+  int blocks;        // ceil(k / 128)
+  size_t code_bytes, scale_bytes, partial_bytes, total_bytes;
+};
+
+// Sizes only: what the workspace query and the launch share. False: refused.
+bool plan_fp8_block(int64_t m, int64_t n, int64_t k, Fp8BlockPlan* p);
+qpn_status check_fp8_block_quantize(const void* x, int32_t dtype, int64_t rows, int64_t k, int64_t stride,
+                                    int32_t block_rows, const uint8_t* codes, int64_t code_stride, const float* scales,
+                                    int64_t scale_row_stride, int64_t scale_block_stride, bool* run);
+qpn_status check_fp8_block_gemm(const qpn_fp8_block_gemm_args* a, const void* ws, size_t ws_bytes, Fp8BlockPlan* p,
+                                bool* run);
+
+}  // namespace qpn

@@ -1,0 +1,79 @@
+"""Binding of the entry points of ``include/qpn_prompt.h`` (8-bit products with
+a scale for each block of 128, attention of a chunk of new tokens over the
+4-bit cache, log-probabilities of given tokens), one for one: integer device
+pointers and sizes in, the qpn_status code checked (a negative one raises
+``QpnError``). ``prompt_api`` has the torch helpers."""
+
+import ctypes
+
+from . import _check
+from . import lib as _base_lib
+
+QPN_DT_E4M3 = 4
+
+_P = ctypes.c_void_p
+_I32 = ctypes.c_int32
+_I64 = ctypes.c_int64
+_SZ = ctypes.c_size_t
+
+
+class qpn_fp8_block_gemm_args(ctypes.Structure):
+    _fields_ = [
+        ("x", _P),
+        ("x_scales", _P),
+        ("w", _P),
+        ("w_scales", _P),
+        ("y", _P),
+        ("x_stride", _I64),
+        ("x_scale_row_stride", _I64),
+        ("x_scale_block_stride", _I64),
+        ("w_stride", _I64),
+        ("w_scale_row_stride", _I64),
+        ("w_scale_block_stride", _I64),
+        ("y_stride", _I64),
+        ("m", _I64),
+        ("n", _I64),
+        ("k", _I64),
+        ("x_dtype", _I32),
+        ("y_dtype", _I32),
+    ]
+
+
+_G = ctypes.POINTER(qpn_fp8_block_gemm_args)
+
+# name -> (restype, argtypes); the declarations of include/qpn_prompt.h
+SIGNATURES = {
+    "qpn_fp8_block_quantize": (_I32, [_P, _I32, _I64, _I64, _I64, _I32, _P, _I64, _P, _I64, _I64, _P]),
+    "qpn_fp8_block_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "qpn_fp8_block_gemm": (_I32, [_G, _P, _SZ, _P]),
+}
+
+_lib = None
+
+
+def lib():
+    """The loaded libqpn.so with these entry points declared."""
+    global _lib
+    if _lib is None:
+        handle = _base_lib()
+        for name, (res, args) in SIGNATURES.items():
+            fn = getattr(handle, name)
+            fn.restype = res
+            fn.argtypes = args
+        _lib = handle
+    return _lib
+
+
+def qpn_fp8_block_quantize(x, dtype, rows, k, stride, block_rows, codes, code_stride, scales, scale_row_stride,
+                           scale_block_stride, stream):
+    return _check(lib().qpn_fp8_block_quantize(x, dtype, rows, k, stride, block_rows, codes, code_stride, scales,
+                                               scale_row_stride, scale_block_stride, stream), "qpn_fp8_block_quantize")
+
+
+def qpn_fp8_block_workspace_bytes(m, n, k):
+    return lib().qpn_fp8_block_workspace_bytes(m, n, k)
+
+
+def qpn_fp8_block_gemm(args, workspace, workspace_bytes, stream):
+    return _check(lib().qpn_fp8_block_gemm(ctypes.byref(args), workspace, workspace_bytes, stream),
+                  "qpn_fp8_block_gemm")

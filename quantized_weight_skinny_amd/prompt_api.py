@@ -1,0 +1,172 @@
+"""Torch plumbing over the entry points of ``include/qpn_prompt.h``: a prompt's
+step, where ``torch_api`` and ``decode_api`` serve steps of up to 16 rows.
+Device memory and the current stream only; every step runs in the library's
+HIP kernels.
+
+    w = BlockWeight(codes, scales)                    # E4M3 and a scale for each 128 x 128, as they are
+    y = fp8_block_linear(x, w)                        # any number of rows
+    out, lse = kv4_chunk_attention(q, k, v, cache, table, kv_len, layer=layer)
+    logprobs, entropy, rank, top, top_logprobs = token_logprobs(logits, tokens, top=5)
+"""
+
+import functools
+
+import torch
+
+from .decode_api import (DTYPES, HALVES, INT32_MAX, _exactly, _on_device, _out, _rows, _sizes, _stream,  # noqa: F401
+                         _workspace)
+from .prompt import (
+    QPN_DT_E4M3,
+    qpn_fp8_block_gemm,
+    qpn_fp8_block_gemm_args,
+    qpn_fp8_block_quantize,
+    qpn_fp8_block_workspace_bytes,
+)
+
+BLOCK = 128  # elements under one scale
+CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _blocks(n):
+    return -(-n // BLOCK)
+
+
+def _matrix(t, name, device, dtypes, shape=None):
+    """A tensor [rows, columns] with contiguous rows any distance apart; returns
+    its address and that distance."""
+    _on_device(t, name, device)
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be one of {', '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must have shape {shape or ('rows', 'columns')}, not {tuple(t.shape)}")
+    rows, columns = t.shape
+    if columns > 1 and t.stride(1) != 1 and t.numel():
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return t.data_ptr(), t.stride(0) if rows > 1 and columns > 0 else columns
+
+
+def _block_scales(t, shape, name, device):
+    """fp32 scales of this shape, any strides; returns address and strides."""
+    _on_device(t, name, device)
+    if t.dtype is not torch.float32 or t.shape != shape:
+        raise ValueError(f"{name} must be a torch.float32 tensor of shape {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else 1, t.stride(1) if shape[1] > 1 else 1
+
+
+def _quantize(x, block_rows, codes, scales):
+    dev = x.device if isinstance(x, torch.Tensor) else None
+    xp, stride = _matrix(x, "x", dev, tuple(DTYPES))
+    rows, k = x.shape
+    if codes is None:
+        codes = torch.empty((rows, -(-k // 16) * 16), dtype=torch.float8_e4m3fn, device=dev)[:, :k]
+    cp, code_stride = _matrix(codes, "codes", dev, CODES, (rows, k))
+    shape = (-(-rows // block_rows), _blocks(k))
+    if scales is None:
+        # a block's scales of neighbouring rows lie together, as the product reads them
+        scales = torch.empty(shape[::-1], dtype=torch.float32, device=dev).t()
+    sp, sr, sb = _block_scales(scales, shape, "scales", dev)
+    qpn_fp8_block_quantize(xp, DTYPES[x.dtype], rows, k, stride, block_rows, cp, code_stride, sp, sr, sb, _stream(dev))
+    return codes, scales
+
+
+def quantize_fp8_rows(x, codes=None, scales=None):
+    """(codes [rows, k] float8_e4m3fn, scales fp32 [rows, ceil(k / 128)]) of x
+    [rows, k] fp16, bf16 or fp32: activations, a scale for each row and 128
+    columns. A scale is the least power of two that takes the block's largest
+    magnitude to 448 or below (1 for zeros), so every code is the E4M3 value
+    nearest to x / scale; inf and NaN get the NaN code. codes may also be uint8;
+    the rows of all three any distance apart, scales with any strides."""
+    return _quantize(x, 1, codes, scales)
+
+
+def quantize_fp8_blocks(w, codes=None, scales=None):
+    """The same for a weight w [n, k], with a scale for each 128 rows and 128
+    columns: scales fp32 [ceil(n / 128), ceil(k / 128)]."""
+    return _quantize(w, BLOCK, codes, scales)
+
+
+class BlockWeight:
+    """A weight [n, k] as E4M3 codes (float8_e4m3fn or uint8; rows a multiple of
+    16 bytes apart and 16-byte aligned, k a multiple of 16) and fp32 scales
+    [ceil(n / 128), ceil(k / 128)], any strides. It keeps both as they are:
+    nothing is copied or laid out anew."""
+
+    def __init__(self, codes, scales):
+        _on_device(codes, "codes")
+        dev = codes.device
+        cp, stride = _matrix(codes, "codes", dev, CODES)
+        n, k = codes.shape
+        if k % 16 or stride % 16 or cp % 16:
+            raise ValueError(f"codes need a number of columns ({k}) and of bytes from row to row ({stride}) that 16 "
+                             "divides, and 16-byte alignment")
+        sp, sr, sb = _block_scales(scales, (_blocks(n), _blocks(k)), "scales", dev)
+        self.codes, self.scales, self.device, self.n, self.k = codes, scales, dev, n, k
+        self._fields = (cp, sp, stride, sr, sb)
+
+    @classmethod
+    def quantize(cls, w):
+        """From w [n, k] fp16, bf16 or fp32 (see quantize_fp8_blocks)."""
+        return cls(*quantize_fp8_blocks(w))
+
+
+_fp8_workspace_bytes = functools.lru_cache(maxsize=256)(qpn_fp8_block_workspace_bytes)
+
+
+def fp8_block_workspace(m, n, k, device="cuda"):
+    """A workspace for fp8_block_linear and fp8_block_gemm with these sizes
+    (None when none is needed). It carries nothing from call to call, but two
+    calls that may run at once need one each."""
+    _sizes(m=m, n=n, k=k)
+    need = _fp8_workspace_bytes(m, n, k)
+    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+
+
+def _product(x, scales, w, dtype, out, workspace):
+    dev = w.device
+    n, k = w.n, w.k
+    coded = scales is not None
+    xp, x_stride = _matrix(x, "codes" if coded else "x", dev, CODES if coded else tuple(DTYPES))
+    m = x.shape[0]
+    if x.shape[1] != k:
+        raise ValueError(f"{'codes' if coded else 'x'} must have shape (rows, {k}), not {tuple(x.shape)}")
+    if coded:
+        if x_stride % 16 or xp % 16:
+            raise ValueError("codes must be 16-byte aligned, with a number of bytes from row to row that 16 divides")
+        sp, sr, sb = _block_scales(scales, (m, _blocks(k)), "scales", dev)
+    else:
+        sp, sr, sb = None, 0, 0
+    if out is None:
+        out = torch.empty(m, n, dtype=dtype, device=dev)
+        yp, y_stride = out.data_ptr(), n
+    else:
+        yp, y_stride = _matrix(out, "out", dev, (dtype,), (m, n))
+    cp, wp, w_stride, wr, wb = w._fields
+    a = qpn_fp8_block_gemm_args(xp, sp, cp, wp, yp, x_stride, sr, sb, w_stride, wr, wb, y_stride, m, n, k,
+                                QPN_DT_E4M3 if coded else DTYPES[x.dtype], DTYPES[dtype])
+    workspace, ws, nbytes = _workspace(_fp8_workspace_bytes(m, n, k), workspace, dev)
+    qpn_fp8_block_gemm(a, ws, nbytes, _stream(dev))
+    return out
+
+
+def _out_dtype(dtype, out, default):
+    if dtype is None:
+        dtype = out.dtype if isinstance(out, torch.Tensor) else default
+    if dtype not in DTYPES:
+        raise ValueError(f"dtype must be one of {', '.join(str(d) for d in DTYPES)}, not {dtype}")
+    return dtype
+
+
+def fp8_block_linear(x, w, dtype=None, out=None, workspace=None):
+    """y [rows, n] = x @ w.T for x [rows, k] fp16, bf16 or fp32 and a
+    BlockWeight: x is quantized as by quantize_fp8_rows, the products of codes
+    are exact, sums fp32, y rounded once to dtype (default: x's). Rows of x and
+    out any distance apart."""
+    _on_device(x, "x")
+    return _product(x, None, w, _out_dtype(dtype, out, x.dtype), out, workspace)
+
+
+def fp8_block_gemm(codes, scales, w, dtype=None, out=None, workspace=None):
+    """The same from codes [rows, k] and scales fp32 [rows, ceil(k / 128)] that
+    are there already (any scales; codes as a BlockWeight's). dtype defaults to
+    bf16."""
+    return _product(codes, scales, w, _out_dtype(dtype, out, torch.bfloat16), out, workspace)

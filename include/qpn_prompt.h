@@ -72,6 +72,61 @@ size_t qpn_fp8_block_workspace_bytes(int64_t m, int64_t n, int64_t k);
 qpn_status qpn_fp8_block_gemm(const qpn_fp8_block_gemm_args* args, void* workspace_dev, size_t workspace_bytes,
                               void* stream);
 
+/* Attention of chunks of new tokens over their sequences' cached tokens and
+ * themselves. Sequence b has kv_len[b] tokens in the 4-bit cache, in pages
+ * table[b * table_stride + t / page_size], and the new tokens q_start[b] ..
+ * q_start[b + 1] - 1 (q_start NULL: max_q_len each) with rows of q, k and v;
+ * their keys and values are read from k and v as they are, and need not have
+ * been appended. Row i sits at position kv_len + i and sees the cached tokens
+ * (position t) and the new ones up to itself, with window > 0 those at
+ * positions above its own less window. Query head h reads kv head
+ * h / (heads / kv_heads).
+ *   out[row][head] = sum_t softmax_t(scale * q . k_t) v_t      (dtype of q)
+ *   lse[row][head] = log sum_t exp(scale * q . k_t)            (fp32, may be NULL)
+ * A page index outside the pool holds no tokens: its positions are not seen.
+ * Tokens that a row does not see have no effect on it, whatever k, v or the
+ * cache hold there. Rows that no sequence has are not written.
+ * All sums are fp32. Rounded to fewer bits are: the softmax weights before
+ * their product with the values, to fp16 for cached tokens and to the type of q
+ * for new ones (each is off by at most half a step of that type, or, in fp16, by 2^-33 of
+ * the row's largest); and, for the cached tokens, q of bf16, which is scaled by
+ * a power of two that takes a row's largest element to 2^15 and then held in
+ * fp16 (elements keep their 8 bits down to 2^-32 of the largest). lse sums the
+ * weights unrounded. Scores are to be below 2^26 in magnitude. */
+typedef struct {
+  const void* q;           /* device: [rows][heads][head_dim] by strides */
+  const void* k;           /* device: [rows][kv_heads][head_dim] by strides */
+  const void* v;
+  void* out;               /* device: contiguous, 16-byte aligned */
+  float* lse;              /* device: [rows][heads], or NULL */
+  const int32_t* table;    /* device: page indices */
+  const int32_t* kv_len;   /* device: [batch], each 0 .. max_kv_len */
+  const int32_t* q_start;  /* device: [batch + 1] from 0 to rows, or NULL */
+  int64_t q_token_stride;  /* elements */
+  int64_t q_head_stride;
+  int64_t k_token_stride;
+  int64_t k_head_stride;
+  int64_t v_token_stride;
+  int64_t v_head_stride;
+  int64_t table_stride;    /* entries a sequence, table_stride * page_size >= max_kv_len */
+  int32_t dtype;           /* F16 or BF16, of q, k, v and out */
+  int32_t layer;
+  int32_t heads;           /* a multiple of kv_heads */
+  int32_t batch;
+  int32_t rows;            /* all sequences' new tokens */
+  int32_t max_q_len;       /* no sequence has more new tokens */
+  int32_t max_kv_len;      /* no sequence has more cached tokens; longer ones are cut there */
+  int32_t window;          /* 0: none */
+  float scale;             /* finite and > 0 */
+  int32_t reserved;        /* 0 */
+} qpn_kv4_chunk_args;
+
+/* Workspace of a call (its pointers may be NULL; 0: none is needed). */
+size_t qpn_kv4_chunk_workspace_bytes(const qpn_kv4_cache* cache, const qpn_kv4_chunk_args* args);
+
+qpn_status qpn_kv4_chunk_attention(const qpn_kv4_cache* cache, const qpn_kv4_chunk_args* args, void* workspace_dev,
+                                   size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -34,4 +34,13 @@ qpn_status qpn_fp8_block_gemm(const qpn_fp8_block_gemm_args* args, void* workspa
   return from_hip(qpn::launch_fp8_block_gemm(*args, plan, workspace_dev, as_stream(stream)));
 }
 
+qpn_status qpn_kv4_chunk_attention(const qpn_kv4_cache* cache, const qpn_kv4_chunk_args* args, void* workspace_dev,
+                                   size_t workspace_bytes, void* stream) {
+  bool run = false;
+  qpn::ChunkPlan plan;
+  const qpn_status st = qpn::check_kv4_chunk(cache, args, workspace_dev, workspace_bytes, &plan, &run);
+  if (st != QPN_OK || !run) return st;
+  return from_hip(qpn::launch_kv4_chunk(*cache, *args, plan, workspace_dev, as_stream(stream)));
+}
+
 }  // extern "C"

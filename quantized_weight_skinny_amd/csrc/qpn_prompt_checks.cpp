@@ -103,9 +103,70 @@ qpn_status check_fp8_block_gemm(const qpn_fp8_block_gemm_args* a, const void* ws
   return QPN_OK;
 }
 
+qpn_status plan_chunk(const qpn_kv4_cache* c, const qpn_kv4_chunk_args* a, ChunkPlan* p) {
+  if (!c || !a || a->reserved != 0) return QPN_ERR_INVALID_ARG;
+  if (qpn_kv4_page_bytes(c->page_size, c->kv_heads, c->head_dim) == 0) return QPN_ERR_INVALID_ARG;
+  if (a->heads < 1 || a->heads > 65536 || a->heads % c->kv_heads != 0) return QPN_ERR_INVALID_ARG;
+  if (a->batch < 0 || a->batch > 65536 || a->rows < 0 || a->rows > (1 << 24) || a->max_q_len < 0 ||
+      a->max_q_len > (1 << 20))
+    return QPN_ERR_INVALID_ARG;
+  // positions and token counts stay inside 32 bits with a step to spare
+  if (a->max_kv_len < 0 || a->max_kv_len > (1 << 30) || a->window < 0) return QPN_ERR_INVALID_ARG;
+  *p = ChunkPlan{};
+  p->splits = 1;
+  if (a->batch == 0 || a->rows == 0) return QPN_OK;
+  const int64_t group = a->heads / c->kv_heads, longest = std::min(a->max_q_len, a->rows);
+  // a row of a sequence is counted in 32 bits
+  if (longest * group > (1 << 30)) return QPN_ERR_UNSUPPORTED;
+  const int64_t tiles = std::min(a->batch * ceil_div(longest * group, kChunkRows), a->rows * group / kChunkRows + a->batch);
+  const int64_t units = tiles * c->kv_heads;
+  if (units * (kChunkRows / 4) > kMaxGroups) return QPN_ERR_UNSUPPORTED;
+  p->tiles = static_cast<int>(tiles);
+  const int64_t steps = ceil_div(a->max_kv_len, kChunkTokens) + ceil_div(longest, kChunkTokens);
+  if (units < 512) p->splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(512 / units, steps / 4)));
+  if (p->splits > 1)
+    p->total_bytes = static_cast<size_t>(units) * p->splits * kChunkRows * (c->head_dim + 2) * sizeof(float);
+  return QPN_OK;
+}
+
+qpn_status check_kv4_chunk(const qpn_kv4_cache* c, const qpn_kv4_chunk_args* a, const void* ws, size_t ws_bytes,
+                           ChunkPlan* p, bool* run) {
+  *run = false;
+  qpn_status st = check_kv4_cache(c);
+  if (st != QPN_OK) return st;
+  st = plan_chunk(c, a, p);
+  if (st != QPN_OK) return st;
+  if (a->layer < 0 || a->layer >= c->layers || !half_type(a->dtype)) return QPN_ERR_INVALID_ARG;
+  if (!isfinite(a->scale) || !(a->scale > 0.0f)) return QPN_ERR_INVALID_ARG;
+  if (!stride_ok(a->q_token_stride) || !stride_ok(a->q_head_stride) || !stride_ok(a->k_token_stride) ||
+      !stride_ok(a->k_head_stride) || !stride_ok(a->v_token_stride) || !stride_ok(a->v_head_stride))
+    return QPN_ERR_INVALID_ARG;
+  if (a->table_stride < 0 || a->table_stride > INT32_MAX) return QPN_ERR_INVALID_ARG;
+  if (a->table_stride * c->page_size < a->max_kv_len) return QPN_ERR_INVALID_ARG;
+  if (!a->q_start && static_cast<int64_t>(a->batch) * a->max_q_len != a->rows) return QPN_ERR_INVALID_ARG;
+  if (a->rows > 0 && a->batch == 0) return QPN_ERR_INVALID_ARG;
+  if (a->batch == 0 || a->rows == 0) return QPN_OK;
+  if (a->max_q_len == 0) return QPN_ERR_INVALID_ARG;
+  if (!a->q || !aligned(a->q, 2) || !a->k || !aligned(a->k, 2) || !a->v || !aligned(a->v, 2)) return QPN_ERR_INVALID_ARG;
+  if (!a->out || !aligned(a->out, 16) || !aligned(a->lse, 4)) return QPN_ERR_INVALID_ARG;
+  if (!a->kv_len || !aligned(a->kv_len, 4) || !aligned(a->q_start, 4)) return QPN_ERR_INVALID_ARG;
+  if (a->max_kv_len > 0 && (!a->table || !aligned(a->table, 4))) return QPN_ERR_INVALID_ARG;
+  if (p->total_bytes > 0) {
+    if (!ws || !aligned(ws, 16)) return QPN_ERR_INVALID_ARG;
+    if (ws_bytes < p->total_bytes) return QPN_ERR_BUFFER_TOO_SMALL;
+  }
+  *run = true;
+  return QPN_OK;
+}
+
 }  // namespace qpn
 
 extern "C" {
+
+size_t qpn_kv4_chunk_workspace_bytes(const qpn_kv4_cache* cache, const qpn_kv4_chunk_args* args) {
+  qpn::ChunkPlan p;
+  return qpn::plan_chunk(cache, args, &p) == QPN_OK ? p.total_bytes : 0;
+}
 
 size_t qpn_fp8_block_workspace_bytes(int64_t m, int64_t n, int64_t k) {
   qpn::Fp8BlockPlan p;

@@ -27,4 +27,18 @@ qpn_status check_fp8_block_quantize(const void* x, int32_t dtype, int64_t rows, 
 qpn_status check_fp8_block_gemm(const qpn_fp8_block_gemm_args* a, const void* ws, size_t ws_bytes, Fp8BlockPlan* p,
                                 bool* run);
 
+constexpr int kChunkRows = 128;   // query rows (tokens x heads of a group) of a workgroup
+constexpr int kChunkTokens = 64;  // tokens it takes at a time
+
+// The shape of a chunk attention.
+struct ChunkPlan {
+  int tiles;   // row tiles of all sequences, at most
+  int splits;  // shares of a tile's tokens, a workgroup each; 1: no join
+  size_t total_bytes;
+};
+
+qpn_status plan_chunk(const qpn_kv4_cache* c, const qpn_kv4_chunk_args* a, ChunkPlan* p);
+qpn_status check_kv4_chunk(const qpn_kv4_cache* c, const qpn_kv4_chunk_args* a, const void* ws, size_t ws_bytes,
+                           ChunkPlan* p, bool* run);
+
 }  // namespace qpn

@@ -13,5 +13,7 @@ hipError_t launch_fp8_block_quantize(const void* x, int32_t dtype, int64_t rows,
                                      int64_t scale_row_stride, int64_t scale_block_stride, hipStream_t stream);
 hipError_t launch_fp8_block_gemm(const qpn_fp8_block_gemm_args& a, const Fp8BlockPlan& p, void* workspace,
                                  hipStream_t stream);
+hipError_t launch_kv4_chunk(const qpn_kv4_cache& c, const qpn_kv4_chunk_args& a, const ChunkPlan& p, void* workspace,
+                            hipStream_t stream);
 
 }  // namespace qpn

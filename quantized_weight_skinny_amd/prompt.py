@@ -8,6 +8,7 @@ import ctypes
 
 from . import _check
 from . import lib as _base_lib
+from .decode import qpn_kv4_cache
 
 QPN_DT_E4M3 = 4
 
@@ -39,13 +40,47 @@ class qpn_fp8_block_gemm_args(ctypes.Structure):
     ]
 
 
+class qpn_kv4_chunk_args(ctypes.Structure):
+    _fields_ = [
+        ("q", _P),
+        ("k", _P),
+        ("v", _P),
+        ("out", _P),
+        ("lse", _P),
+        ("table", _P),
+        ("kv_len", _P),
+        ("q_start", _P),
+        ("q_token_stride", _I64),
+        ("q_head_stride", _I64),
+        ("k_token_stride", _I64),
+        ("k_head_stride", _I64),
+        ("v_token_stride", _I64),
+        ("v_head_stride", _I64),
+        ("table_stride", _I64),
+        ("dtype", _I32),
+        ("layer", _I32),
+        ("heads", _I32),
+        ("batch", _I32),
+        ("rows", _I32),
+        ("max_q_len", _I32),
+        ("max_kv_len", _I32),
+        ("window", _I32),
+        ("scale", ctypes.c_float),
+        ("reserved", _I32),
+    ]
+
+
+_C = ctypes.POINTER(qpn_kv4_cache)
 _G = ctypes.POINTER(qpn_fp8_block_gemm_args)
+_A = ctypes.POINTER(qpn_kv4_chunk_args)
 
 # name -> (restype, argtypes); the declarations of include/qpn_prompt.h
 SIGNATURES = {
     "qpn_fp8_block_quantize": (_I32, [_P, _I32, _I64, _I64, _I64, _I32, _P, _I64, _P, _I64, _I64, _P]),
     "qpn_fp8_block_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
     "qpn_fp8_block_gemm": (_I32, [_G, _P, _SZ, _P]),
+    "qpn_kv4_chunk_workspace_bytes": (_SZ, [_C, _A]),
+    "qpn_kv4_chunk_attention": (_I32, [_C, _A, _P, _SZ, _P]),
 }
 
 _lib = None
@@ -77,3 +112,12 @@ def qpn_fp8_block_workspace_bytes(m, n, k):
 def qpn_fp8_block_gemm(args, workspace, workspace_bytes, stream):
     return _check(lib().qpn_fp8_block_gemm(ctypes.byref(args), workspace, workspace_bytes, stream),
                   "qpn_fp8_block_gemm")
+
+
+def qpn_kv4_chunk_workspace_bytes(cache, args):
+    return lib().qpn_kv4_chunk_workspace_bytes(ctypes.byref(cache), ctypes.byref(args))
+
+
+def qpn_kv4_chunk_attention(cache, args, workspace, workspace_bytes, stream):
+    return _check(lib().qpn_kv4_chunk_attention(ctypes.byref(cache), ctypes.byref(args), workspace, workspace_bytes,
+                                                stream), "qpn_kv4_chunk_attention")

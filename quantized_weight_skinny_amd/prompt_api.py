@@ -15,12 +15,16 @@ import torch
 
 from .decode_api import (DTYPES, HALVES, INT32_MAX, _exactly, _on_device, _out, _rows, _sizes, _stream,  # noqa: F401
                          _workspace)
+from .decode import qpn_kv4_cache
 from .prompt import (
     QPN_DT_E4M3,
     qpn_fp8_block_gemm,
     qpn_fp8_block_gemm_args,
     qpn_fp8_block_quantize,
     qpn_fp8_block_workspace_bytes,
+    qpn_kv4_chunk_args,
+    qpn_kv4_chunk_attention,
+    qpn_kv4_chunk_workspace_bytes,
 )
 
 BLOCK = 128  # elements under one scale
@@ -170,3 +174,81 @@ def fp8_block_gemm(codes, scales, w, dtype=None, out=None, workspace=None):
     are there already (any scales; codes as a BlockWeight's). dtype defaults to
     bf16."""
     return _product(codes, scales, w, _out_dtype(dtype, out, torch.bfloat16), out, workspace)
+
+
+@functools.lru_cache(maxsize=256)
+def _chunk_workspace_bytes(page_size, kv_heads, head_dim, rows, heads, batch, max_q_len, max_kv_len):
+    c = qpn_kv4_cache(None, 0, 1, page_size, kv_heads, head_dim, 1.0, 1.0)
+    a = qpn_kv4_chunk_args()
+    a.heads, a.batch, a.rows, a.max_q_len, a.max_kv_len = heads, batch, rows, max_q_len, max_kv_len
+    return qpn_kv4_chunk_workspace_bytes(c, a)
+
+
+def kv4_chunk_workspace(cache, rows, heads, batch, max_q_len, max_kv_len):
+    """A workspace for kv4_chunk_attention with these sizes (None when none is
+    needed). It carries nothing from call to call, but two calls that may run
+    at once need one each."""
+    _sizes(rows=rows, heads=heads, batch=batch, max_q_len=max_q_len, max_kv_len=max_kv_len)
+    need = _chunk_workspace_bytes(cache.page_size, cache.kv_heads, cache.head_dim, rows, heads, batch, max_q_len,
+                                  max_kv_len)
+    return torch.empty(need, dtype=torch.uint8, device=cache.device) if need else None
+
+
+def kv4_chunk_attention(q, k, v, cache, table, kv_len, q_start=None, max_q_len=None, max_kv_len=None, layer=0,
+                        scale=None, window=0, out=None, lse=None, workspace=None):
+    """(out, lse): attention of each sequence's new tokens over its cached
+    tokens and themselves, causal.
+
+    q [rows, heads, head_dim], k and v [rows, kv_heads, head_dim], fp16 or bf16
+    (any strides with a contiguous last dimension: slices of a fused
+    projection's output will do). The new tokens' keys and values are read from
+    k and v as they are, so they may be appended before or after; table int32
+    [batch, pages a sequence at most] and kv_len int32 [batch] are of the tokens
+    that were cached before (table may have no columns). q_start int32 [batch +
+    1] from 0 to rows, with max_q_len the longest (None: rows / batch rows
+    each); max_kv_len bounds the lengths (default: what the table can hold).
+    window > 0: a row sees the last `window` tokens up to its own. out [rows,
+    heads, head_dim] like q, lse fp32 [rows, heads]. What is rounded to fewer bits is in
+    qpn_prompt.h; sums are fp32."""
+    dev = cache.device
+    dim, kv_heads = cache.head_dim, cache.kv_heads
+    _on_device(q, "q", dev)
+    if q.dim() != 3:
+        raise ValueError(f"q must have shape (rows, heads, {dim}), not {tuple(q.shape)}")
+    rows, heads, _ = q.shape
+    qp, qt, qh = _rows(q, (rows, heads, dim), "q", dev, HALVES)
+    kp, kt, kh = _rows(k, (rows, kv_heads, dim), "k", dev, (q.dtype,))
+    vp, vt, vh = _rows(v, (rows, kv_heads, dim), "v", dev, (q.dtype,))
+    if heads == 0 or heads % kv_heads:
+        raise ValueError(f"q's {heads} heads must be a multiple of the cache's {kv_heads}")
+    _on_device(table, "table", dev)
+    if table.dtype is not torch.int32 or table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError("table must be an int32 [batch, pages] tensor with contiguous rows")
+    batch, pages = table.shape
+    lp = _exactly(kv_len, torch.int32, (batch,), "kv_len", dev)
+    if q_start is not None:
+        sp = _exactly(q_start, torch.int32, (batch + 1,), "q_start", dev)
+        if max_q_len is None:
+            raise ValueError("q_start needs max_q_len, the longest sequence's rows")
+    else:
+        sp = None
+        each = rows // batch if batch else 0
+        if each * batch != rows or (max_q_len is not None and max_q_len != each):
+            raise ValueError(f"{rows} rows are not {batch} sequences of as many: give q_start and max_q_len")
+        max_q_len = each
+    if max_kv_len is None:
+        max_kv_len = pages * cache.page_size
+    if not (0 <= window <= INT32_MAX and 0 <= max_q_len <= INT32_MAX and 0 <= max_kv_len <= INT32_MAX):
+        raise ValueError(f"window {window}, max_q_len {max_q_len} and max_kv_len {max_kv_len} must be 0 .. {INT32_MAX}")
+    if max_kv_len > pages * cache.page_size:   # (a slice's rows may lie further apart than they are long)
+        raise ValueError(f"max_kv_len {max_kv_len} is more than a table row's {pages} pages of {cache.page_size} hold")
+    out = _out(out, q.dtype, (rows, heads, dim), "out", dev)
+    lse = _out(lse, torch.float32, (rows, heads), "lse", dev)
+    a = qpn_kv4_chunk_args(qp, kp, vp, out.data_ptr(), lse.data_ptr(), table.data_ptr(), lp, sp, qt, qh, kt, kh, vt, vh,
+                           table.stride(0) if batch > 1 and pages > 0 else pages, DTYPES[q.dtype], layer, heads, batch,
+                           rows, max_q_len, max_kv_len, window, dim ** -0.5 if scale is None else scale, 0)
+    workspace, wp, nbytes = _workspace(
+        _chunk_workspace_bytes(cache.page_size, kv_heads, dim, rows, heads, batch, max_q_len, max_kv_len), workspace,
+        dev)
+    qpn_kv4_chunk_attention(cache.desc(layer), a, wp, nbytes, _stream(dev))
+    return out, lse

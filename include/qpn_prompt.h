@@ -127,6 +127,40 @@ size_t qpn_kv4_chunk_workspace_bytes(const qpn_kv4_cache* cache, const qpn_kv4_c
 qpn_status qpn_kv4_chunk_attention(const qpn_kv4_cache* cache, const qpn_kv4_chunk_args* args, void* workspace_dev,
                                    size_t workspace_bytes, void* stream);
 
+/* Log-probabilities of given tokens. With x a row's logits, t its temperature
+ * and p = softmax(x / t):
+ *   logprobs[row]     = log p[token]
+ *   entropy[row]      = -sum p log p
+ *   rank[row]         = how many tokens come before the given one
+ *   top_tokens[row]   = the first `top` tokens, and top_logprobs their log p
+ * where tokens with larger logits come first, equal ones in the order of their
+ * index. A token outside 0 .. vocab - 1 gives 0 and a rank of -1. NaN logits
+ * count as -inf. Infinite logits share p = 1 among themselves; a row of -inf
+ * alone gives log p = -inf and an entropy of 0. A temperature that is 0, below
+ * or NaN counts as 1. Sums are fp32 over a few elements of a row and 64 bits
+ * beyond. */
+typedef struct {
+  const void* logits;        /* device: [rows][vocab], rows row_stride elements apart */
+  const int32_t* tokens;     /* device: [rows], or NULL with logprobs and rank NULL */
+  const float* temperature;  /* device: [rows], or NULL (1) */
+  float* logprobs;           /* device: [rows], may be NULL */
+  float* entropy;            /* device: [rows], may be NULL */
+  int32_t* rank;             /* device: [rows], may be NULL */
+  int32_t* top_tokens;       /* device: [rows][top], NULL only if top is 0 */
+  float* top_logprobs;       /* device: [rows][top], NULL only if top is 0 */
+  int64_t row_stride;        /* elements */
+  int32_t dtype;             /* F16, BF16 or F32 */
+  int32_t rows;              /* 0 .. 2^20 */
+  int32_t vocab;             /* 1 .. 2^24 */
+  int32_t top;               /* 0 .. 64, at most vocab */
+} qpn_logprobs_args;
+
+/* Workspace of a call with these sizes (0: none is needed, or refused sizes). */
+size_t qpn_token_logprobs_workspace_bytes(int32_t rows, int32_t vocab, int32_t top);
+
+qpn_status qpn_token_logprobs(const qpn_logprobs_args* args, void* workspace_dev, size_t workspace_bytes,
+                              void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -14,7 +14,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SOURCES = ["qpn_api.hip", "qpn_gemm.hip", "qpn_mlp.hip", "qpn_pack.hip", "qpn_plan.cpp", "qpn_checks.cpp",
            "qpn_decode_api.hip", "qpn_kv4_attention.hip", "qpn_kv4_cache.hip", "qpn_verify.hip",
-           "qpn_decode_checks.cpp", "qpn_prompt_api.hip", "qpn_fp8_block.hip", "qpn_kv4_chunk.hip",
+           "qpn_decode_checks.cpp", "qpn_prompt_api.hip", "qpn_fp8_block.hip", "qpn_kv4_chunk.hip", "qpn_logprobs.hip",
            "qpn_prompt_checks.cpp"]
 LIB = os.path.join(HERE, "libqpn.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -1,0 +1,469 @@
+// Log-probabilities of given tokens, entropies and the first tokens of rows of
+// logits (include/qpn_prompt.h).
+//
+// Mathematics. With f = log2(e) / t and a reference m, a lane keeps
+// s = sum 2^((x - m) f) and w = sum 2^((x - m) f) (x - m) f over its elements in
+// one pass; a larger m' scales them by d = 2^((m - m') f), after w has been
+// given (m - m') f times s. Then log2 p = (x - m) f - log2 s, and the entropy
+// is log2 s - w / s, both times ln 2. Lanes, wavefronts and slices of a row are
+// added in 64 bits.
+//
+// The first tokens are found in the same pass. Every wavefront keeps a list of
+// candidates above a bound of its own, which at least `top` of the elements it has
+// seen reach; a wavefront's elements come in the order of their index, so a
+// later one that equals the bound comes after these. The first bound is the
+// top-th largest of the lanes' maxima over the first 2048 elements: some
+// (vocabulary / 8192) * top candidates follow for one wavefront of a row of no
+// order, and the list is cut back to `top` (by a search over the keys' bits,
+// with votes) when it passes 128, which raises the bound. Rising rows, whose
+// every element passes, cost more and are no less right.
+#include "qpn_decode_internal.hpp"
+#include "qpn_device.hpp"
+#include "qpn_prompt_internal.hpp"
+
+namespace qpn {
+namespace {
+
+constexpr int kThreads = 256, kWaves = kThreads / 64;
+constexpr int kEach = kLogprobsStep / kThreads;  // elements a lane takes at a time
+constexpr int kList = 128;               // candidates that a wavefront keeps
+constexpr int kAtOnce = 8 * 64;          // ... and what it may add before it looks
+constexpr int kKeys = (kList + kAtOnce) / 64;
+typedef u4 u4_anywhere __attribute__((aligned(2)));
+constexpr float kLowest = -3.402823466e38f;
+
+struct Stat {
+  double sum, dot;  // s and w under the reference max
+  float max;
+  int before;       // elements that come before the given token
+};
+static_assert(sizeof(Stat) == 24, "the workspace holds 24 bytes a slice");
+
+struct LogprobsParams {
+  qpn_logprobs_args a;
+  int slices, length;  // of a row, and a slice's elements
+  Stat* stats;         // [rows][slices]
+  uint64_t* lists;     // [rows][slices][top]: keys in descending order, 0 past the last
+};
+
+struct Bf16 {
+  uint16_t bits;
+};
+template <typename T>
+__device__ __forceinline__ float widen(T x) {
+  if constexpr (sizeof(T) == 4) return x;
+  else if constexpr (__is_same(T, Bf16)) return widen16<true>(x.bits);
+  else return static_cast<float>(x);
+}
+
+// A lane's 16 bytes of elements as fp32.
+template <typename T>
+__device__ __forceinline__ void widen_piece(const u4& w, float* x) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(w[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[2 * e] = widen16<__is_same(T, Bf16)>(w[e] & 0xFFFFu);
+      x[2 * e + 1] = widen16<__is_same(T, Bf16)>(w[e] >> 16);
+    }
+  }
+}
+
+// Larger keys come first: the logit's order (-0 as 0, NaN as -inf), then the lower index.
+__device__ __forceinline__ uint32_t order_of(float x) {
+  const uint32_t b = __float_as_uint(x == x ? x + 0.0f : -__builtin_inff());
+  return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t order) {
+  return __uint_as_float(order ^ ((order & 0x80000000u) ? 0x80000000u : 0xFFFFFFFFu));
+}
+__device__ __forceinline__ uint64_t key_of(float x, int index) {
+  return static_cast<uint64_t>(order_of(x)) << 32 | ~static_cast<uint32_t>(index);
+}
+constexpr uint32_t kMinusInf = 0x007FFFFFu;  // order_of(-inf)
+
+// Cuts a wavefront's list of n keys (all different) back to the `top` largest,
+// top <= n; returns the order of the smallest that stays.
+__device__ __forceinline__ uint32_t cut_list(uint64_t* list, int& n, int top) {
+  const int lane = threadIdx.x & 63;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // the list holds other lanes' keys
+  uint64_t key[kKeys];
+#pragma unroll
+  for (int j = 0; j < kKeys; ++j) key[j] = j * 64 + lane < n ? list[j * 64 + lane] : 0;
+  // the largest bound that `top` keys reach, in the upper half, then in the lower among its equals
+  uint64_t bound = 0;
+#pragma unroll 1
+  for (int bit = 63; bit >= 32; --bit) {
+    const uint64_t next = bound | uint64_t(1) << bit;
+    int count = 0;
+#pragma unroll
+    for (int j = 0; j < kKeys; ++j) count += __popcll(__ballot(static_cast<uint32_t>(key[j] >> 32) >= static_cast<uint32_t>(next >> 32)));
+    if (count >= top) bound = next;
+  }
+  int reach = 0;
+#pragma unroll
+  for (int j = 0; j < kKeys; ++j) reach += __popcll(__ballot(key[j] >= bound));
+  if (reach > top) {
+#pragma unroll 1
+    for (int bit = 31; bit >= 0; --bit) {
+      const uint64_t next = bound | uint64_t(1) << bit;
+      int count = 0;
+#pragma unroll
+      for (int j = 0; j < kKeys; ++j) count += __popcll(__ballot(key[j] >= next));
+      if (count >= top) bound = next;
+    }
+  }
+  int at = 0;
+#pragma unroll
+  for (int j = 0; j < kKeys; ++j) {
+    const uint64_t stays = __ballot(key[j] >= bound);
+    const int mine = at + __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(stays >> 32),
+                                                    __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(stays), 0));
+    if (key[j] >= bound) list[mine] = key[j];
+    at += __popcll(stays);
+  }
+  n = at;
+  return static_cast<uint32_t>(bound >> 32);
+}
+
+// Adds the lanes' keys where `take` to the wavefront's list.
+__device__ __forceinline__ void add_keys(uint64_t* list, int& n, bool take, uint64_t key) {
+  const uint64_t all = __ballot(take);
+  if (take)
+    list[n + __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(all >> 32),
+                                       __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(all), 0))] = key;
+  n += __popcll(all);
+}
+
+// The wavefronts' lists (counts[w] keys each) as one, in descending order: `put`
+// gets each key among the first `top` and its place. Returns how many there are.
+template <typename Put>
+__device__ __forceinline__ int merge_lists(const uint64_t (*lists)[kList + kAtOnce], const int* counts, int top, Put put) {
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) total += counts[w];
+#pragma unroll 1
+  for (int mine = threadIdx.x; mine < total; mine += kThreads) {
+    int w = 0, at = mine;
+    while (at >= counts[w]) at -= counts[w++];
+    const uint64_t key = lists[w][at];
+    int place = 0;
+#pragma unroll 1
+    for (int o = 0; o < kWaves; ++o) {
+      const int n = counts[o];
+#pragma unroll 8
+      for (int j = 0; j < n; ++j) place += lists[o][j] > key;
+    }
+    if (place < top) put(key, place);
+  }
+  return min(total, top);
+}
+
+__device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) x = fmaxf(x, __shfl_xor(x, o));
+  return x;
+}
+__device__ __forceinline__ double wave_add(double x) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) x += __shfl_xor(x, o);
+  return x;
+}
+
+__device__ __forceinline__ float factor_of(const LogprobsParams& p, int row) {
+  const float t = p.a.temperature ? p.a.temperature[row] : 1.0f;
+  return fminf(1.44269504088896341f / (t > 0.f ? t : 1.0f), -kLowest);
+}
+
+// 2^((x - m) f), and the exponent: 0 for x of -inf and NaN, whatever m and f.
+__device__ __forceinline__ float weight(float x, float m, float f, float& t) {
+  t = fmaxf((x - m) * f, -1000.0f);
+  return __builtin_amdgcn_exp2f(t);
+}
+
+// s and w under another reference, d = (m - m') f of 0 or below (2^-1000 is 0).
+template <typename F>
+__device__ __forceinline__ void move_reference(F& s, F& w, float d) {
+  d = fmaxf(d, -1000.0f);  // (also of inf - inf)
+  const float down = __builtin_amdgcn_exp2f(d);
+  w = down > 0.f ? (w + s * d) * down : F(0);
+  s *= down;
+}
+
+// One slice of one row.
+template <typename T, bool TOP>
+__global__ __launch_bounds__(kThreads) void logprobs_slices_kernel(const LogprobsParams p) {
+  constexpr int kPiece = 16 / sizeof(T), kPieces = kEach / kPiece;
+  __shared__ Stat joined[kWaves];
+  __shared__ uint64_t lists[TOP ? kWaves : 1][kList + kAtOnce];
+  __shared__ int counts[kWaves];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+  const int row = blockIdx.x / p.slices, slice = blockIdx.x - row * p.slices;
+  const T* x0 = static_cast<const T*>(p.a.logits) + row * p.a.row_stride;
+  const int begin = slice * p.length, end = min(begin + p.length, p.a.vocab);
+  const float f = factor_of(p, row);
+  const int token = p.a.tokens ? p.a.tokens[row] : -1;
+  const bool given = token >= 0 && token < p.a.vocab;
+  // An element comes before the token where it is at least the token's logit
+  // (in front of it) or larger (behind it).
+  float reach = __builtin_inff(), above = __builtin_inff();
+  if (given) {
+    reach = value_of(order_of(widen<T>(x0[token])));
+    above = reach == __builtin_inff() ? __builtin_nanf("") : value_of(order_of(reach) + 1);
+    // (of -inf, all in front: the rows' kernel adds them, NaN among them)
+    if (reach == -__builtin_inff()) reach = __builtin_nanf("");
+  }
+  float m = kLowest, s = 0.f, w = 0.f;
+  int before = 0, n = 0;
+  float bound = -__builtin_inff();
+  bool first = true;
+  uint64_t* list = lists[TOP ? wave : 0];
+
+  u4 raw[kPieces];
+  const auto load = [&](int at) {
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      const int e0 = at + j * 64 * kPiece + lane * kPiece;
+      if (e0 + kPiece <= end) raw[j] = *reinterpret_cast<const u4_anywhere*>(x0 + e0);
+    }
+  };
+  constexpr int kWaveStep = kEach * 64;
+  const int at0 = begin + wave * kWaveStep;
+  if (at0 < end) load(at0);
+  for (int at = at0; at < end; at += kWaveStep * kWaves) {
+    float x[kEach];
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) widen_piece<T>(raw[j], &x[j * kPiece]);
+    if (at + kWaveStep > end) {
+      // the end of the slice: what is past it is -inf, a piece across it comes one by one
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) {
+        const int e0 = at + j * 64 * kPiece + lane * kPiece;
+        if (e0 + kPiece > end) {
+#pragma unroll
+          for (int e = 0; e < kPiece; ++e) x[j * kPiece + e] = e0 + e < end ? widen<T>(x0[e0 + e]) : -__builtin_inff();
+        }
+      }
+    }
+    if (at + kWaveStep * kWaves < end) load(at + kWaveStep * kWaves);
+    float top = m;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) top = fmaxf(top, x[e]);
+    if (__any(top > m)) {
+      move_reference(s, w, (m - top) * f);
+      m = top;
+    }
+    const auto index = [&](int e) { return at + e / kPiece * (64 * kPiece) + lane * kPiece + e % kPiece; };
+    const bool mixed = token >= at && token < at + kWaveStep;
+    const float least = at > token ? above : reach;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      float t;
+      const float y = weight(x[e], m, f, t);
+      s += y;
+      w = fmaf(y, t, w);
+    }
+    if (mixed) {
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) before += x[e] >= (index(e) >= token ? above : reach);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) before += x[e] >= least;
+    }
+    if constexpr (TOP) {
+      float most = x[0];
+#pragma unroll
+      for (int e = 1; e < kEach; ++e) most = fmaxf(most, x[e]);
+      bool equal = false;  // elements that equal the bound count
+      if (first) {
+        // the upper 16 bits of the top-th largest of the lanes' maxima
+        const uint32_t mine = order_of(most);
+        uint32_t b = 0;
+#pragma unroll 1
+        for (int bit = 31; bit >= 16; --bit) {
+          const uint32_t next = b | 1u << bit;
+          if (static_cast<int>(__popcll(__ballot(mine >= next))) >= p.a.top) b = next;
+        }
+        if (b > kMinusInf) bound = value_of(b), equal = true;
+        first = false;
+      }
+      if (__any(equal ? most >= bound : most > bound)) {
+#pragma unroll 1
+        for (int part = 0; part < kEach / 8; ++part) {
+          // (the eight elements of a part lie in front of the next part's for all lanes)
+          float y[8];
+#pragma unroll
+          for (int e = 0; e < kEach; ++e)
+            if (e / 8 == part) y[e % 8] = x[e];
+          float z = y[0];
+#pragma unroll
+          for (int e = 1; e < 8; ++e) z = fmaxf(z, y[e]);
+          if (!__any(equal ? z >= bound : z > bound)) continue;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const bool take = equal ? y[e] >= bound : y[e] > bound;
+            if (__any(take)) add_keys(list, n, take, key_of(y[e], index(part * 8 + e)));
+          }
+          if (n > kList) {
+            bound = value_of(cut_list(list, n, p.a.top));
+            equal = false;
+          }
+        }
+      }
+    }
+  }
+
+  // Lanes, then wavefronts.
+  const float most = wave_max(m);
+  move_reference(s, w, (m - most) * f);
+  const double sum = wave_add(s), dot = wave_add(w);
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) before += __shfl_xor(before, o);
+  if (lane == 0) {
+    joined[wave] = Stat{sum, dot, most, before};
+    counts[wave] = n;
+  }
+  __syncthreads();
+  const int64_t at = static_cast<int64_t>(row) * p.slices + slice;
+  if (threadIdx.x == 0) {
+    Stat r = joined[0];
+#pragma unroll
+    for (int o = 1; o < kWaves; ++o) {
+      Stat y = joined[o];
+      const float top = fmaxf(r.max, y.max);
+      move_reference(r.sum, r.dot, (r.max - top) * f);
+      move_reference(y.sum, y.dot, (y.max - top) * f);
+      r = Stat{r.sum + y.sum, r.dot + y.dot, top, r.before + y.before};
+    }
+    p.stats[at] = r;
+  }
+  if constexpr (TOP) {
+    uint64_t* out = p.lists + at * p.a.top;
+    const int found = merge_lists(lists, counts, p.a.top, [&](uint64_t key, int place) { out[place] = key; });
+    for (int j = found + threadIdx.x; j < p.a.top; j += kThreads) out[j] = 0;
+  }
+}
+
+// A row's slices as one, and its results.
+template <typename T, bool TOP>
+__global__ __launch_bounds__(kThreads) void logprobs_rows_kernel(const LogprobsParams p) {
+  __shared__ uint64_t lists[TOP ? kWaves : 1][kList + kAtOnce];
+  __shared__ int counts[kWaves], infinite;
+  __shared__ uint64_t first[TOP ? 64 : 1];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+  const int row = blockIdx.x;
+  const T* x0 = static_cast<const T*>(p.a.logits) + row * p.a.row_stride;
+  const float f = factor_of(p, row);
+  if (threadIdx.x == 0) infinite = 0;
+  // every wavefront adds all slices
+  Stat r{0.0, 0.0, kLowest, 0};
+  for (int c = lane; c < p.slices; c += 64) {
+    Stat y = p.stats[static_cast<int64_t>(row) * p.slices + c];
+    const float top = fmaxf(r.max, y.max);
+    move_reference(r.sum, r.dot, (r.max - top) * f);
+    move_reference(y.sum, y.dot, (y.max - top) * f);
+    r = Stat{r.sum + y.sum, r.dot + y.dot, top, r.before + y.before};
+  }
+  const float most = wave_max(r.max);
+  move_reference(r.sum, r.dot, (r.max - most) * f);
+  r.sum = wave_add(r.sum), r.dot = wave_add(r.dot), r.max = most;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) r.before += __shfl_xor(r.before, o);
+  if constexpr (TOP) {
+    const uint64_t* in = p.lists + static_cast<int64_t>(row) * p.slices * p.a.top;
+    const int total = p.slices * p.a.top;
+    int n = 0;
+    uint64_t bound = 0;
+    for (int j0 = wave * 64; j0 < total; j0 += kThreads) {
+      const uint64_t key = j0 + lane < total ? in[j0 + lane] : 0;
+      if (__any(key > bound)) add_keys(lists[wave], n, key > bound, key);
+      if (n > kList) bound = static_cast<uint64_t>(cut_list(lists[wave], n, p.a.top)) << 32;
+    }
+    if (lane == 0) counts[wave] = n;
+  }
+  __syncthreads();
+  if (r.max == __builtin_inff()) {
+    // infinite logits share the probability
+    int count = 0;
+    for (int e = threadIdx.x; e < p.a.vocab; e += kThreads) count += widen<T>(x0[e]) == __builtin_inff();
+    if (count) atomicAdd(&infinite, count);
+    __syncthreads();
+    r.sum = infinite, r.dot = 0.0;
+  }
+  // log p = ((x - max) / t) - ln s
+  const float given_t = p.a.temperature ? p.a.temperature[row] : 1.0f;
+  const double t = given_t > 0.f ? given_t : 1.0f, log_sum = r.sum > 0.0 ? log(r.sum) : 0.0;
+  const auto log_p = [&](float x) -> float {
+    if (!(x > -__builtin_inff())) return -__builtin_inff();
+    if (x == r.max) return static_cast<float>(-log_sum);
+    return static_cast<float>((static_cast<double>(x) - static_cast<double>(r.max)) / t - log_sum);
+  };
+  if (threadIdx.x == 0) {
+    const int token = p.a.tokens ? p.a.tokens[row] : -1;
+    const bool given = token >= 0 && token < p.a.vocab;
+    const float x = given ? widen<T>(x0[token]) : 0.f;
+    if (p.a.logprobs) p.a.logprobs[row] = given ? log_p(x) : 0.f;
+    // (all in front of a logit of -inf or NaN come before it)
+    if (p.a.rank) p.a.rank[row] = given ? r.before + (x > -__builtin_inff() ? 0 : token) : -1;
+    if (p.a.entropy) p.a.entropy[row] = r.sum > 0.0 ? static_cast<float>(fmax(log_sum - r.dot / r.sum * 0.69314718055994530942, 0.0)) : 0.f;
+  }
+  if constexpr (TOP) {
+    const int found = merge_lists(lists, counts, p.a.top, [&](uint64_t key, int place) { first[place] = key; });
+    // fewer tokens than asked for are above -inf: the others in the order of their index
+    if (found < p.a.top && wave == 0) {
+      int n = found;
+      for (int e0 = 0; e0 < p.a.vocab && n < p.a.top; e0 += 64) {
+        const bool low = e0 + lane < p.a.vocab && !(widen<T>(x0[e0 + lane]) > -__builtin_inff());
+        const uint64_t all = __ballot(low);
+        const int place = n + __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(all >> 32),
+                                                        __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(all), 0));
+        if (low && place < p.a.top) first[place] = key_of(-__builtin_inff(), e0 + lane);
+        n += __popcll(all);
+      }
+    }
+    __syncthreads();
+    for (int j = threadIdx.x; j < p.a.top; j += kThreads) {
+      const int64_t at = static_cast<int64_t>(row) * p.a.top + j;
+      p.a.top_tokens[at] = static_cast<int32_t>(~static_cast<uint32_t>(first[j]));
+      p.a.top_logprobs[at] = log_p(value_of(static_cast<uint32_t>(first[j] >> 32)));
+    }
+  }
+}
+
+template <typename T>
+hipError_t launch_as(const LogprobsParams& p, hipStream_t stream) {
+  const dim3 grid(static_cast<uint32_t>(p.a.rows) * p.slices), rows(static_cast<uint32_t>(p.a.rows));
+  if (p.a.top > 0) {
+    logprobs_slices_kernel<T, true><<<grid, dim3(kThreads), 0, stream>>>(p);
+  } else {
+    logprobs_slices_kernel<T, false><<<grid, dim3(kThreads), 0, stream>>>(p);
+  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (p.a.top > 0) {
+    logprobs_rows_kernel<T, true><<<rows, dim3(kThreads), 0, stream>>>(p);
+  } else {
+    logprobs_rows_kernel<T, false><<<rows, dim3(kThreads), 0, stream>>>(p);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_token_logprobs(const qpn_logprobs_args& a, const LogprobsPlan& plan, void* workspace,
+                                 hipStream_t stream) {
+  LogprobsParams p;
+  p.a = a;
+  p.slices = plan.slices, p.length = plan.length;
+  p.stats = static_cast<Stat*>(workspace);
+  p.lists = reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(workspace) + plan.stat_bytes);
+  switch (a.dtype) {
+    case QPN_DT_F16: return launch_as<_Float16>(p, stream);
+    case QPN_DT_BF16: return launch_as<Bf16>(p, stream);
+    default: return launch_as<float>(p, stream);
+  }
+}
+
+}  // namespace qpn

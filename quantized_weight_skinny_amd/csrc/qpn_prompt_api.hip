@@ -43,4 +43,13 @@ qpn_status qpn_kv4_chunk_attention(const qpn_kv4_cache* cache, const qpn_kv4_chu
   return from_hip(qpn::launch_kv4_chunk(*cache, *args, plan, workspace_dev, as_stream(stream)));
 }
 
+qpn_status qpn_token_logprobs(const qpn_logprobs_args* args, void* workspace_dev, size_t workspace_bytes,
+                              void* stream) {
+  bool run = false;
+  qpn::LogprobsPlan plan;
+  const qpn_status st = qpn::check_token_logprobs(args, workspace_dev, workspace_bytes, &plan, &run);
+  if (st != QPN_OK || !run) return st;
+  return from_hip(qpn::launch_token_logprobs(*args, plan, workspace_dev, as_stream(stream)));
+}
+
 }  // extern "C"

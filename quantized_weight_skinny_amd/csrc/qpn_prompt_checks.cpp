@@ -159,9 +159,48 @@ qpn_status check_kv4_chunk(const qpn_kv4_cache* c, const qpn_kv4_chunk_args* a, 
   return QPN_OK;
 }
 
+bool plan_logprobs(int32_t rows, int32_t vocab, int32_t top, LogprobsPlan* p) {
+  if (rows < 0 || rows > (1 << 20) || vocab < 1 || vocab > (1 << 24) || top < 0 || top > 64 || top > vocab) return false;
+  *p = LogprobsPlan{};
+  // as many slices as bring 2048 workgroups, 8 for each compute unit
+  const int64_t wanted = rows > 0 ? ceil_div(2048, rows) : 1;
+  const int64_t most = std::min<int64_t>(ceil_div(vocab, kLogprobsStep), kLogprobsSlices);
+  const int64_t length = ceil_div(ceil_div(vocab, std::min(wanted, most)), kLogprobsStep) * kLogprobsStep;
+  p->length = static_cast<int>(length);
+  p->slices = static_cast<int>(ceil_div(vocab, length));
+  p->stat_bytes = round256(static_cast<size_t>(rows) * p->slices * 24);
+  p->total_bytes = rows == 0 ? 0 : p->stat_bytes + static_cast<size_t>(rows) * p->slices * top * 8;
+  return true;
+}
+
+qpn_status check_token_logprobs(const qpn_logprobs_args* a, const void* ws, size_t ws_bytes, LogprobsPlan* p,
+                                bool* run) {
+  *run = false;
+  if (!a) return QPN_ERR_INVALID_ARG;
+  if (!plan_logprobs(a->rows, a->vocab, a->top, p)) return QPN_ERR_INVALID_ARG;
+  if (!half_type(a->dtype) && a->dtype != QPN_DT_F32) return QPN_ERR_INVALID_ARG;
+  if (!stride_ok(a->row_stride)) return QPN_ERR_INVALID_ARG;
+  if (!a->tokens && (a->logprobs || a->rank)) return QPN_ERR_INVALID_ARG;
+  if (a->rows == 0) return QPN_OK;
+  if (!a->logits || !aligned(a->logits, type_size(a->dtype))) return QPN_ERR_INVALID_ARG;
+  if (!aligned(a->tokens, 4) || !aligned(a->temperature, 4) || !aligned(a->logprobs, 4) || !aligned(a->entropy, 4) ||
+      !aligned(a->rank, 4) || !aligned(a->top_tokens, 4) || !aligned(a->top_logprobs, 4))
+    return QPN_ERR_INVALID_ARG;
+  if (a->top > 0 && (!a->top_tokens || !a->top_logprobs)) return QPN_ERR_INVALID_ARG;
+  if (!ws || !aligned(ws, 16)) return QPN_ERR_INVALID_ARG;
+  if (ws_bytes < p->total_bytes) return QPN_ERR_BUFFER_TOO_SMALL;
+  *run = true;
+  return QPN_OK;
+}
+
 }  // namespace qpn
 
 extern "C" {
+
+size_t qpn_token_logprobs_workspace_bytes(int32_t rows, int32_t vocab, int32_t top) {
+  qpn::LogprobsPlan p;
+  return qpn::plan_logprobs(rows, vocab, top, &p) ? p.total_bytes : 0;
+}
 
 size_t qpn_kv4_chunk_workspace_bytes(const qpn_kv4_cache* cache, const qpn_kv4_chunk_args* args) {
   qpn::ChunkPlan p;

@@ -41,4 +41,17 @@ qpn_status plan_chunk(const qpn_kv4_cache* c, const qpn_kv4_chunk_args* a, Chunk
 qpn_status check_kv4_chunk(const qpn_kv4_cache* c, const qpn_kv4_chunk_args* a, const void* ws, size_t ws_bytes,
                            ChunkPlan* p, bool* run);
 
+constexpr int kLogprobsStep = 8192;   // elements of a row that a workgroup takes at a time
+constexpr int kLogprobsSlices = 128;  // slices of a row, at most
+
+// The shape of token log-probabilities: every row in `slices` of `length`.
+struct LogprobsPlan {
+  int slices, length;
+  size_t stat_bytes, total_bytes;
+};
+
+bool plan_logprobs(int32_t rows, int32_t vocab, int32_t top, LogprobsPlan* p);
+qpn_status check_token_logprobs(const qpn_logprobs_args* a, const void* ws, size_t ws_bytes, LogprobsPlan* p,
+                                bool* run);
+
 }  // namespace qpn

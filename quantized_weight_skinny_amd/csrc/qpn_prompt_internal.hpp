@@ -15,5 +15,7 @@ hipError_t launch_fp8_block_gemm(const qpn_fp8_block_gemm_args& a, const Fp8Bloc
                                  hipStream_t stream);
 hipError_t launch_kv4_chunk(const qpn_kv4_cache& c, const qpn_kv4_chunk_args& a, const ChunkPlan& p, void* workspace,
                             hipStream_t stream);
+hipError_t launch_token_logprobs(const qpn_logprobs_args& a, const LogprobsPlan& p, void* workspace,
+                                 hipStream_t stream);
 
 }  // namespace qpn

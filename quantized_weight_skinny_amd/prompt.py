@@ -70,9 +70,28 @@ class qpn_kv4_chunk_args(ctypes.Structure):
     ]
 
 
+class qpn_logprobs_args(ctypes.Structure):
+    _fields_ = [
+        ("logits", _P),
+        ("tokens", _P),
+        ("temperature", _P),
+        ("logprobs", _P),
+        ("entropy", _P),
+        ("rank", _P),
+        ("top_tokens", _P),
+        ("top_logprobs", _P),
+        ("row_stride", _I64),
+        ("dtype", _I32),
+        ("rows", _I32),
+        ("vocab", _I32),
+        ("top", _I32),
+    ]
+
+
 _C = ctypes.POINTER(qpn_kv4_cache)
 _G = ctypes.POINTER(qpn_fp8_block_gemm_args)
 _A = ctypes.POINTER(qpn_kv4_chunk_args)
+_L = ctypes.POINTER(qpn_logprobs_args)
 
 # name -> (restype, argtypes); the declarations of include/qpn_prompt.h
 SIGNATURES = {
@@ -81,6 +100,8 @@ SIGNATURES = {
     "qpn_fp8_block_gemm": (_I32, [_G, _P, _SZ, _P]),
     "qpn_kv4_chunk_workspace_bytes": (_SZ, [_C, _A]),
     "qpn_kv4_chunk_attention": (_I32, [_C, _A, _P, _SZ, _P]),
+    "qpn_token_logprobs_workspace_bytes": (_SZ, [_I32, _I32, _I32]),
+    "qpn_token_logprobs": (_I32, [_L, _P, _SZ, _P]),
 }
 
 _lib = None
@@ -121,3 +142,12 @@ def qpn_kv4_chunk_workspace_bytes(cache, args):
 def qpn_kv4_chunk_attention(cache, args, workspace, workspace_bytes, stream):
     return _check(lib().qpn_kv4_chunk_attention(ctypes.byref(cache), ctypes.byref(args), workspace, workspace_bytes,
                                                 stream), "qpn_kv4_chunk_attention")
+
+
+def qpn_token_logprobs_workspace_bytes(rows, vocab, top):
+    return lib().qpn_token_logprobs_workspace_bytes(rows, vocab, top)
+
+
+def qpn_token_logprobs(args, workspace, workspace_bytes, stream):
+    return _check(lib().qpn_token_logprobs(ctypes.byref(args), workspace, workspace_bytes, stream),
+                  "qpn_token_logprobs")

@@ -25,6 +25,9 @@ from .prompt import (
     qpn_kv4_chunk_args,
     qpn_kv4_chunk_attention,
     qpn_kv4_chunk_workspace_bytes,
+    qpn_logprobs_args,
+    qpn_token_logprobs,
+    qpn_token_logprobs_workspace_bytes,
 )
 
 BLOCK = 128  # elements under one scale
@@ -252,3 +255,44 @@ def kv4_chunk_attention(q, k, v, cache, table, kv_len, q_start=None, max_q_len=N
         dev)
     qpn_kv4_chunk_attention(cache.desc(layer), a, wp, nbytes, _stream(dev))
     return out, lse
+
+
+_logprobs_workspace_bytes = functools.lru_cache(maxsize=256)(qpn_token_logprobs_workspace_bytes)
+
+
+def token_logprobs_workspace(rows, vocab, top=0, device="cuda"):
+    """A workspace for token_logprobs with these sizes. It carries nothing from
+    call to call, but two calls that may run at once need one each."""
+    _sizes(rows=rows, vocab=vocab, top=top)
+    need = _logprobs_workspace_bytes(rows, vocab, top)
+    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+
+
+def token_logprobs(logits, tokens, top=0, temperature=None, logprobs=None, entropy=None, rank=None, top_tokens=None,
+                   top_logprobs=None, workspace=None):
+    """(logprobs fp32 [rows], entropy fp32 [rows], rank int32 [rows], top_tokens
+    int32 [rows, top], top_logprobs fp32 [rows, top]) of logits [rows, vocab]
+    (fp16, bf16 or fp32, rows any distance apart) at tokens int32 [rows].
+
+    With p = softmax(logits / temperature) (fp32 [rows]; None, 0 or below: 1):
+    log p of the given token (0 for one outside the vocabulary), the entropy of
+    p, how many tokens come before the given one (-1), and the first `top` (0
+    to 64) tokens. Larger logits come first, equal ones in the order of their
+    index; NaN counts as -inf."""
+    _on_device(logits, "logits")
+    dev = logits.device
+    xp, stride = _matrix(logits, "logits", dev, tuple(DTYPES))
+    rows, vocab = logits.shape
+    _sizes(rows=rows, vocab=vocab, top=top)
+    tp = _exactly(tokens, torch.int32, (rows,), "tokens", dev)
+    fp = None if temperature is None else _exactly(temperature, torch.float32, (rows,), "temperature", dev)
+    logprobs = _out(logprobs, torch.float32, (rows,), "logprobs", dev)
+    entropy = _out(entropy, torch.float32, (rows,), "entropy", dev)
+    rank = _out(rank, torch.int32, (rows,), "rank", dev)
+    top_tokens = _out(top_tokens, torch.int32, (rows, top), "top_tokens", dev)
+    top_logprobs = _out(top_logprobs, torch.float32, (rows, top), "top_logprobs", dev)
+    a = qpn_logprobs_args(xp, tp, fp, logprobs.data_ptr(), entropy.data_ptr(), rank.data_ptr(), top_tokens.data_ptr(),
+                          top_logprobs.data_ptr(), stride, DTYPES[logits.dtype], rows, vocab, top)
+    workspace, wp, nbytes = _workspace(_logprobs_workspace_bytes(rows, vocab, top), workspace, dev)
+    qpn_token_logprobs(a, wp, nbytes, _stream(dev))
+    return logprobs, entropy, rank, top_tokens, top_logprobs

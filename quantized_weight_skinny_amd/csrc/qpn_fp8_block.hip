@@ -312,7 +312,7 @@ __global__ __launch_bounds__(MW * NW * 64, 2) void many_rows_kernel(const Produc
   constexpr int kStage = (kM + kN) * kScaleBlock, kLoads = kStage / 16 / kThreads;
   static_assert(kStage % (16 * kThreads) == 0 && kM * 8 % kThreads == 0, "whole loads of either operand");
   static_assert(kScaleBlock % (TN * 16) == 0, "a wavefront's outputs share their scale");
-  __shared__ uint8_t lds[2][kStage];  // x rows, then w rows
+  __shared__ alignas(16) uint8_t lds[2][kStage];  // x rows, then w rows
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i = lane & 15, g = lane >> 4;
   const int64_t m_tiles = (p.m + kM - 1) / kM;

@@ -118,8 +118,8 @@ __device__ __forceinline__ uint32_t scaled_pair(uint32_t w, h2 s) {
 template <int DIM>
 struct Tiles {
   static constexpr int kKeyStride = DIM + 8;
-  uint16_t k[kTokens * kKeyStride];
-  uint16_t v[DIM * kTokens];
+  alignas(16) uint16_t k[kTokens * kKeyStride];
+  alignas(16) uint16_t v[DIM * kTokens];
   uint32_t odd[2];  // new tokens of the tile whose values hold inf or NaN
 };
 

@@ -34,6 +34,7 @@ typedef __bf16 b2 __attribute__((ext_vector_type(2)));
 typedef u4 u4_anywhere __attribute__((aligned(2)));
 
 constexpr int kThreads = 256, kRows = kChunkRows, kTokens = kChunkTokens;
+constexpr int kMinShare = 4;        // steps a share has at least
 constexpr float kNoToken = -1e30f;  // a row's reference before it has seen a token
 constexpr float kBias = 8.0f, kHeadroom = 15.0f;
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
@@ -49,54 +50,109 @@ struct ChunkParams {
   const int32_t* table;
   int64_t table_stride;
   const int32_t *kv_len, *q_start;
-  int32_t batch, rows, max_q, max_kv, window, tiles, splits;
+  int32_t batch, rows, max_q, max_kv, window, tiles, groups;
   float f, k_scale, v_scale;  // f: scale * log2(e)
-  float* part;                // [tiles * kv_heads * splits][kRows][DIM], then [..][kRows][2]
+  struct Cut* cuts;           // [groups]; groups 0: a workgroup a run, no join
+  float* part;                // [2 groups][kRows][DIM], then [2 groups][kRows][2]
 };
 
-// A row tile: rows row0 .. of those of sequence b, whose new tokens are qs ..
-// qs + ql - 1 and which has `len` cached ones.
-struct RowTile {
-  int b, qs, ql, len, row0;
+// The run that a workgroup's share begins inside of (rows 0: it begins with
+// one): its pieces are those of shares first .. last, its rows `rows` of kv
+// head `head`'s from row `row0` of the sequence whose new tokens begin at `qs`.
+struct Cut {
+  int rows, first, last, qs, row0, head, pad[2];
+};
+static_assert(sizeof(Cut) == 32, "the workspace holds 32 bytes a share");
+
+// A sequence: its new tokens qs .. qs + ql - 1, its `len` cached ones, its row
+// tiles and what they cost: row tile j first + more * j, in sixteenths of a step of
+// 64 tokens.
+struct Sequence {
+  int qs, ql, len, tiles, first, more;
 };
 
-__device__ __forceinline__ void new_tokens(const ChunkParams& a, int b, int& qs, int& ql) {
+// What a run costs besides its steps, in steps: queries, the first loads, the output.
+constexpr int kRunCost = 3;
+
+__device__ __forceinline__ Sequence sequence(const ChunkParams& a, int b) {
+  Sequence s;
   if (a.q_start) {
-    qs = min(max(a.q_start[b], 0), a.rows);
-    ql = min(min(max(a.q_start[b + 1] - qs, 0), a.max_q), a.rows - qs);
+    s.qs = min(max(a.q_start[b], 0), a.rows);
+    s.ql = min(min(max(a.q_start[b + 1] - s.qs, 0), a.max_q), a.rows - s.qs);
   } else {
-    qs = b * a.max_q;
-    ql = a.max_q;
+    s.qs = b * a.max_q;
+    s.ql = a.max_q;
   }
+  s.len = a.pages > 0 ? min(max(a.kv_len[b], 0), a.max_kv) : 0;
+  s.tiles = (s.ql * a.group + kRows - 1) / kRows;
+  // a window's row tile sees the window and its own rows, another all cached tokens and the new ones up to it
+  const int seen = a.window ? min(a.window + kRows / a.group, s.len + s.ql) : s.len;
+  s.first = 16 * (seen / kTokens + 1 + kRunCost);
+  s.more = a.window ? 0 : 16 * kRows / kTokens / a.group;
+  return s;
 }
 
-// Tile `t` of all sequences' row tiles laid end to end (false: there are fewer).
-__device__ __forceinline__ bool find_tile(const ChunkParams& a, int t, RowTile& r) {
+// The cost of the first j row tiles.
+__device__ __forceinline__ int64_t cost_of(const Sequence& s, int64_t j) {
+  return s.first * j + s.more * (j * (j - 1) / 2);
+}
+
+__device__ __forceinline__ Sequence lane_of(const Sequence& s, int l) {
+  const auto get = [&](int x) { return __builtin_amdgcn_readlane(x, l); };
+  return Sequence{get(s.qs), get(s.ql), get(s.len), get(s.tiles), get(s.first), get(s.more)};
+}
+
+__device__ __forceinline__ int64_t lane_of(int64_t x, int l) {
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(x), l);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(static_cast<uint64_t>(x) >> 32), l);
+  return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+// Sums over the lanes up to each.
+__device__ __forceinline__ int64_t scan(int64_t x) {
   const int lane = threadIdx.x & 63;
-  int before = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += 64) {
-    int qs = 0, ql = 0;
-    if (b0 + lane < a.batch) new_tokens(a, b0 + lane, qs, ql);
-    const int mine = static_cast<int>((static_cast<int64_t>(ql) * a.group + kRows - 1) / kRows);
-    int sum = mine;
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int x = __shfl_up(sum, o);
-      if (lane >= o) sum += x;
+  for (int o = 1; o < 64; o <<= 1) {
+    const int64_t y = __shfl_up(x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+// Where place `at` of a line lies to which sequence b adds line(sequence): the
+// sequence and the place at which its part begins (false: behind the line).
+template <typename Line>
+__device__ __forceinline__ bool find_sequence(const ChunkParams& a, int64_t at, Line line, int& b, int64_t& base,
+                                              Sequence& s) {
+  const int lane = threadIdx.x & 63;
+  int64_t before = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += 64) {
+    Sequence mine = {0, 0, 0, 0, 0, 0};
+    int64_t part = 0;
+    if (b0 + lane < a.batch) {
+      mine = sequence(a, b0 + lane);
+      part = line(mine);
     }
-    const uint64_t past = __ballot(t < before + sum);
+    const int64_t sum = scan(part);
+    const uint64_t past = __ballot(at < before + sum);
     if (past) {
       const int l = __builtin_ctzll(past);
-      r.b = b0 + l;
-      r.qs = __builtin_amdgcn_readlane(qs, l);
-      r.ql = __builtin_amdgcn_readlane(ql, l);
-      r.row0 = (t - before - __builtin_amdgcn_readlane(sum, l) + __builtin_amdgcn_readlane(mine, l)) * kRows;
-      r.len = a.pages > 0 ? min(max(a.kv_len[r.b], 0), a.max_kv) : 0;
+      b = b0 + l;
+      base = before + lane_of(sum - part, l);
+      s = lane_of(mine, l);
       return true;
     }
-    before += __builtin_amdgcn_readlane(sum, 63);
+    before += lane_of(sum, 63);
   }
   return false;
+}
+
+// The kernel's arguments, to be read again from where they lie.
+typedef const ChunkParams __attribute__((address_space(4))) * ParamsPtr;
+__device__ __forceinline__ const ChunkParams& reread(const ChunkParams&) {
+  ParamsPtr p = (ParamsPtr)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const ChunkParams*)p;
 }
 
 __device__ __forceinline__ h2 splat(_Float16 x) { return h2{x, x}; }
@@ -164,7 +220,7 @@ __device__ __forceinline__ bool strike_odd(uint32_t& x) {
 }
 
 template <int DIM, bool BF16>
-__global__ __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) void kv4_chunk_kernel(const ChunkParams a) {
+__global__ __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) void kv4_chunk_kernel(const ChunkParams params) {
   constexpr int kSteps = DIM / 16, kBlocks = DIM / 32;
   constexpr int kKeyUnits = (kTokens * DIM / 32 + kThreads - 1) / kThreads;  // of 32 elements, a thread
   constexpr int kPerToken = DIM / 32;
@@ -173,16 +229,79 @@ __global__ __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) void kv4_chunk_kernel
   constexpr int kNewQuads = kTokens / 4 * DIM / 8 / kThreads; // 8 elements of four new tokens' values, a thread
   constexpr int kQuadUnits = kNewQuads > 0 ? kNewQuads : 1;
   __shared__ Tiles<DIM> sh;
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int i = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+  int tid = threadIdx.x, lane = tid & 63;
 
-  const int head = blockIdx.x % a.kv_heads, rest = blockIdx.x / a.kv_heads;
-  const int split = rest % a.splits;
-  const int tile = a.tiles - 1 - rest / a.splits;  // a sequence's last rows, which see most, go first
-  RowTile rt;
-  if (!find_tile(a, tile, rt)) return;
+  // The work is the steps of all (sequence, kv head, row tile), laid end to end in
+  // that order. Each of `groups` workgroups, as many as the device holds at once,
+  // takes an equal share of that line, whatever the lengths: a share may begin inside
+  // of one run of steps and end inside another. A run that lies in one share is written
+  // as it is; the pieces of any other go to the workspace, at most two a share (the end
+  // of a run in slot 2 w, the beginning of one in slot 2 w + 1), and the join kernel adds
+  // them. Workgroups go round the eight dies; each die takes an eighth of the line, so
+  // that the row tiles of a head, which read the same tokens, meet in its cache.
+  int b = 0, share_of = 0;
+  int64_t base = 0, at = 0, end = 1, share = 0;
+  Sequence seq;
+  {
+  const ChunkParams& a = params;
+  if (a.groups == 0) {
+    const int64_t t = a.tiles - 1 - blockIdx.x / a.kv_heads;  // a sequence's last rows, which see most, go first
+    if (!find_sequence(a, t, [](const Sequence& x) { return static_cast<int64_t>(x.tiles); }, b, base, seq)) return;
+    at = (blockIdx.x % a.kv_heads) * cost_of(seq, seq.tiles) + cost_of(seq, t - base);
+    end = at + seq.first + seq.more * (t - base);
+    base = 0;
+  } else {
+    const auto line = [&](const Sequence& x) { return a.kv_heads * cost_of(x, x.tiles); };
+    int64_t total = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 64) {
+      int64_t part = 0;
+      if (b0 + lane < a.batch) part = line(sequence(a, b0 + lane));
+      total += lane_of(scan(part), 63);
+    }
+    share_of = blockIdx.x % 8 * (a.groups / 8) + blockIdx.x / 8;
+    share = max((total + a.groups - 1) / a.groups, static_cast<int64_t>(16 * kMinShare));
+    at = share_of * share;
+    end = min(at + share, total);
+    if (at >= total) {
+      if (tid == 0) a.cuts[share_of].rows = 0;
+      return;
+    }
+    find_sequence(a, at, line, b, base, seq);
+  }
+  }
+  bool first_run = true;
+  while (true) {
+  // (what follows from the lane is worked out again for every run: kept from one
+  // to the next it would take registers; and so are the arguments, which come from
+  // the scalar cache)
+  asm volatile("" : "+v"(tid), "+v"(lane));
+  const ChunkParams& a = reread(params);
+  const int i = lane & 31, h = lane >> 5;
+  // The run: its kv head and row tile, and the part [from, to) of its cost.
+  const int64_t head_cost = cost_of(seq, seq.tiles);
+  const int head = static_cast<int>((at - base) / head_cost);
+  const int64_t in_head = at - base - head * head_cost;
+  int low = 0, high = seq.tiles - 1;  // the last row tile that begins at in_head or before
+  while (low < high) {
+    const int mid = (low + high + 1) / 2;
+    if (cost_of(seq, mid) <= in_head) low = mid;
+    else high = mid - 1;
+  }
+  const int cost = seq.first + seq.more * low;
+  const int from = static_cast<int>(in_head - cost_of(seq, low));
+  const int to = static_cast<int>(min(static_cast<int64_t>(cost), from + end - at));
+  struct { int b, qs, ql, len, row0; } rt = {b, seq.qs, seq.ql, seq.len, low * kRows};
   const int nrows = min(rt.ql * a.group - rt.row0, kRows);
   const int win = a.window;
+  const bool alone = from == 0 && to == cost;
+  if (first_run && a.groups && tid == 0) {
+    const int64_t begin = at - from;
+    a.cuts[share_of] = Cut{from > 0 ? nrows : 0, static_cast<int>(begin / share),
+                           static_cast<int>((begin + cost - 1) / share), rt.qs, rt.row0, head, {0, 0}};
+  }
+  first_run = false;
+  at += to - from;
 
   // The tokens that the tile's rows see, in steps of 64: cached ones from step
   // c0 to c1, then new ones from n0 to n1.
@@ -193,8 +312,8 @@ __global__ __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) void kv4_chunk_kernel
     n0 = max(q_first - win + 1, 0) / kTokens;
   }
   const int steps = c1 - c0 + n1 - n0;
-  const int s0 = static_cast<int>(static_cast<int64_t>(steps) * split / a.splits);
-  const int s1 = static_cast<int>(static_cast<int64_t>(steps) * (split + 1) / a.splits);
+  const int s0 = static_cast<int>(static_cast<int64_t>(steps) * from / cost);
+  const int s1 = static_cast<int>(static_cast<int64_t>(steps) * to / cost);
   // this workgroup's share of them
   const int cb = c0 + min(s0, c1 - c0), ce = c0 + min(s1, c1 - c0);
   const int nb = n0 + max(s0 - (c1 - c0), 0), ne = n0 + max(s1 - (c1 - c0), 0);
@@ -226,12 +345,15 @@ __global__ __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) void kv4_chunk_kernel
 #pragma unroll
     for (int x = 0; x < 2; ++x) s[x] = 0.f;
 #pragma unroll
-    for (int c = 0; c < kSteps; ++c)
+    for (int c = 0; c < kSteps; ++c) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const u4 key = *reinterpret_cast<const u4*>(&sh.k[(x * 32 + i) * Tiles<DIM>::kKeyStride + c * 16 + h * 8]);
         s[x] = H::mfma(key, q[c], s[x]);
       }
+      // (else the compiler asks for all keys at once, and has no registers for them)
+      if (DIM == 256 && c % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+    }
     if (!whole) {
       const uint64_t mine = held >> (4 * h);
       const int from = lo - 4 * h, to = hi - 4 * h;
@@ -270,13 +392,15 @@ __global__ __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) void kv4_chunk_kernel
         p[x * 2 + e / 8][e % 8 / 2] = H::round2(p0, p1);
       }
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+    for (int c = 0; c < 4; ++c) {
 #pragma unroll
       for (int n = 0; n < kBlocks; ++n) {
         const int d = n * 32 + i;
         const u4 val = *reinterpret_cast<const u4*>(&sh.v[d * kTokens + (((2 * c + h) ^ ((d ^ (d >> 3)) & 7)) * 8)]);
         o[n] = H::mfma(val, p[c], o[n]);
       }
+      if (DIM == 256) __builtin_amdgcn_sched_barrier(0);
+    }
   };
 
   // ---- cached tokens
@@ -417,13 +541,15 @@ __global__ __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) void kv4_chunk_kernel
     const uint16_t* kb = static_cast<const uint16_t*>(a.k) + rt.qs * a.k_ts + head * a.k_hs;
     const uint16_t* vb = static_cast<const uint16_t*>(a.v) + rt.qs * a.v_ts + head * a.v_hs;
     u4 kn[kNewUnits], vn[kQuadUnits][4];
-    const auto load_new = [&](int c) {
+    const auto load_new_keys = [&](int c) {
       // (tokens past the last are the last again: no row sees them)
 #pragma unroll
       for (int j = 0; j < kNewUnits; ++j) {
         const int unit = j * kThreads + tid, t = min(c * kTokens + unit / (DIM / 8), rt.ql - 1);
         kn[j] = *reinterpret_cast<const u4_anywhere*>(kb + t * a.k_ts + unit % (DIM / 8) * 8);
       }
+    };
+    const auto load_new_values = [&](int c) {
 #pragma unroll
       for (int j = 0; j < kQuadUnits; ++j) {
         const int unit = min(j * kThreads + tid, kTokens / 4 * DIM / 8 - 1);
@@ -434,13 +560,15 @@ __global__ __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) void kv4_chunk_kernel
         }
       }
     };
-    // `guard`: some row may not see some token of these, so their values must be finite
-    const auto store_new = [&](bool guard) {
+    const auto store_new_keys = [&] {
 #pragma unroll
       for (int j = 0; j < kNewUnits; ++j) {
         const int unit = j * kThreads + tid;
         *reinterpret_cast<u4*>(&sh.k[unit / (DIM / 8) * Tiles<DIM>::kKeyStride + unit % (DIM / 8) * 8]) = kn[j];
       }
+    };
+    // `guard`: some row may not see some token of these, so their values must be finite
+    const auto store_new_values = [&](bool guard) {
 #pragma unroll
       for (int j = 0; j < kQuadUnits; ++j) {
         const int unit = j * kThreads + tid, qd = unit / (DIM / 8), d = unit % (DIM / 8) * 8;
@@ -471,16 +599,30 @@ __global__ __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) void kv4_chunk_kernel
       }
     };
     constexpr bool kAhead = DIM < 256;  // (heads of 256 have no registers left for the next tokens)
-    if constexpr (kAhead) load_new(nb);
+    if constexpr (kAhead) {
+      load_new_keys(nb);
+      load_new_values(nb);
+    }
     load_queries();
     if (tid < 2) sh.odd[tid] = 0;
     __syncthreads();
     for (int c = nb; c < ne; ++c) {
       const int t0 = c * kTokens;
       const bool guard = t0 + kTokens - 1 > q_first || (win != 0 && t0 <= q_last - win);
-      if constexpr (!kAhead) load_new(c);
-      store_new(guard);
-      if (kAhead && c + 1 < ne) load_new(c + 1);
+      if constexpr (kAhead) {
+        store_new_keys();
+        store_new_values(guard);
+        if (c + 1 < ne) {
+          load_new_keys(c + 1);
+          load_new_values(c + 1);
+        }
+      } else {
+        load_new_keys(c);
+        store_new_keys();
+        __builtin_amdgcn_sched_barrier(0);
+        load_new_values(c);
+        store_new_values(guard);
+      }
       __syncthreads();
       const uint32_t odd0 = sh.odd[0], odd1 = sh.odd[1];
       if (busy) {
@@ -509,91 +651,97 @@ __global__ __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) void kv4_chunk_kernel
     }
   }
 
-  if (!busy) return;
-  l += __shfl_xor(l, 32);
-  if (!live) return;
-  if (a.splits > 1) {
-    const int64_t slot = (static_cast<int64_t>(tile) * a.kv_heads + head) * a.splits + split;
-    const int64_t slots = static_cast<int64_t>(a.tiles) * a.kv_heads * a.splits;
-    if (h == 0) *reinterpret_cast<float2*>(a.part + slots * kRows * DIM + (slot * kRows + r) * 2) = float2{m, l};
-    if (s0 == s1) return;
-    float* dst = a.part + (slot * kRows + r) * DIM + 4 * h;
+  if (busy) {
+    l += __shfl_xor(l, 32);
+    const int64_t row_at = static_cast<int64_t>(rt.qs + qi) * (a.kv_heads * a.group) + head * a.group + hh;
+    if (live && !alone) {
+      const int64_t slot = (2 * share_of + (from == 0)) * kRows + r;
+      if (h == 0) reinterpret_cast<float2*>(a.part + static_cast<int64_t>(2 * a.groups) * kRows * DIM)[slot] = float2{m, l};
+      float* dst = a.part + slot * DIM + 4 * h;
 #pragma unroll
-    for (int n = 0; n < kBlocks; ++n)
+      for (int n = 0; n < kBlocks; ++n)
 #pragma unroll
-      for (int e = 0; e < 16; e += 4)
-        *reinterpret_cast<f4*>(dst + n * 32 + e * 2) = f4{o[n][e], o[n][e + 1], o[n][e + 2], o[n][e + 3]};
-    return;
+        for (int e = 0; e < 16; e += 4)
+          *reinterpret_cast<f4*>(dst + n * 32 + e * 2) = f4{o[n][e], o[n][e + 1], o[n][e + 2], o[n][e + 3]};
+    } else if (live) {
+      const float up = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+      uint16_t* dst = static_cast<uint16_t*>(a.out) + row_at * DIM + 4 * h;
+#pragma unroll
+      for (int n = 0; n < kBlocks; ++n)
+#pragma unroll
+        for (int e = 0; e < 16; e += 4)
+          *reinterpret_cast<uint2*>(dst + n * 32 + e * 2) = uint2{Half<BF16>::round2(o[n][e] * up, o[n][e + 1] * up),
+                                                                  Half<BF16>::round2(o[n][e + 2] * up, o[n][e + 3] * up)};
+      if (h == 0 && a.lse) a.lse[row_at] = l == 0.f ? -__builtin_inff() : (__builtin_amdgcn_logf(l) + m) * kLn2;
+    }
   }
-  const int64_t row_at = static_cast<int64_t>(rt.qs + qi) * (a.kv_heads * a.group) + head * a.group + hh;
-  const float up = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-  uint16_t* dst = static_cast<uint16_t*>(a.out) + row_at * DIM + 4 * h;
-#pragma unroll
-  for (int n = 0; n < kBlocks; ++n)
-#pragma unroll
-    for (int e = 0; e < 16; e += 4)
-      *reinterpret_cast<uint2*>(dst + n * 32 + e * 2) = uint2{Half<BF16>::round2(o[n][e] * up, o[n][e + 1] * up),
-                                                              Half<BF16>::round2(o[n][e + 2] * up, o[n][e + 3] * up)};
-  if (h == 0 && a.lse) a.lse[row_at] = l == 0.f ? -__builtin_inff() : (__builtin_amdgcn_logf(l) + m) * kLn2;
+  if (at >= end) break;
+  if (at - base >= a.kv_heads * head_cost) {
+    // the next sequence that has rows
+    base = at;
+    do seq = sequence(a, ++b);
+    while (seq.tiles == 0);
+  }
+  }
 }
 
-// Joins the pieces of a row, in the order of the tokens, a wavefront a row.
-constexpr int kJoinWaves = 4;
+// Joins the pieces of the runs that were cut, in the order of the line, a
+// wavefront a row: a run of n + 1 pieces has n shares that begin inside of it, and
+// these share its rows.
+constexpr int kJoinWaves = 16;
 
 template <int DIM, bool BF16>
 __global__ __launch_bounds__(kJoinWaves * 64) void kv4_chunk_join_kernel(const ChunkParams a) {
-  constexpr int kLanes = DIM / 4, kGroups = 64 / kLanes;  // lanes that hold a row, four elements each; rows of pieces at once
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
-  constexpr int kParts = kRows / kJoinWaves;
-  const int part = blockIdx.x % kParts, unit = blockIdx.x / kParts;  // unit: tile * kv_heads + head
-  const int tile = unit / a.kv_heads, head = unit - tile * a.kv_heads;
-  RowTile rt;
-  if (!find_tile(a, tile, rt)) return;
-  const int r = part * kJoinWaves + wave;
-  if (r >= min(rt.ql * a.group - rt.row0, kRows)) return;
+  constexpr int kLanes = DIM / 4, kAtOnce = 64 / kLanes;  // lanes that hold a row, four elements each; pieces at once
+  const int lane = threadIdx.x & 63, w = blockIdx.x;
+  const Cut c = a.cuts[w];
+  if (c.rows == 0) return;  // else first < w <= last
   const int gr = lane / kLanes, d = lane % kLanes * 4;
-  const int64_t slots = static_cast<int64_t>(a.tiles) * a.kv_heads * a.splits, slot0 = static_cast<int64_t>(unit) * a.splits;
-  const float2* ml = reinterpret_cast<const float2*>(a.part + slots * kRows * DIM);
-  float mx = kNoToken, l = 0.f;
-  f4 v = {0.f, 0.f, 0.f, 0.f};
+  const float2* ml = reinterpret_cast<const float2*>(a.part + static_cast<int64_t>(2 * a.groups) * kRows * DIM);
+  const int n = c.last - c.first;
+  for (int r = w - c.first - 1 + __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6) * n; r < c.rows;
+       r += n * kJoinWaves) {
+    float mx = kNoToken, l = 0.f;
+    f4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-  for (int s = gr; s < a.splits; s += kGroups) {
-    const float2 x = ml[(slot0 + s) * kRows + r];
-    if (x.y == 0.f) continue;  // a piece of no seen tokens
-    const f4 piece = *reinterpret_cast<const f4*>(a.part + ((slot0 + s) * kRows + r) * DIM + d);
-    const float top = fmaxf(mx, x.x), down = __builtin_amdgcn_exp2f(mx - top), p = __builtin_amdgcn_exp2f(x.x - top);
-    mx = top;
-    l = l * down + p * x.y;
-    v = v * down + piece * p;
+    for (int x = c.first + gr; x <= c.last; x += kAtOnce) {
+      const int64_t slot = (2 * x + (x == c.first)) * static_cast<int64_t>(kRows) + r;
+      const float2 q = ml[slot];
+      const f4 piece = *reinterpret_cast<const f4*>(a.part + slot * DIM + d);
+      const float top = fmaxf(mx, q.x), down = __builtin_amdgcn_exp2f(mx - top), p = __builtin_amdgcn_exp2f(q.x - top);
+      mx = top;
+      l = l * down + p * q.y;
+      v = v * down + piece * p;
+    }
+    const float own = mx;
+#pragma unroll
+    for (int o = kLanes; o < 64; o <<= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
+    const float down = __builtin_amdgcn_exp2f(own - mx);
+    l *= down;
+    v *= down;
+#pragma unroll
+    for (int o = kLanes; o < 64; o <<= 1) {
+      l += __shfl_xor(l, o);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += __shfl_xor(v[e], o);
+    }
+    if (gr != 0) continue;
+    const int qi = (c.row0 + r) / a.group, hh = c.row0 + r - qi * a.group;
+    const int64_t row_at = static_cast<int64_t>(c.qs + qi) * (a.kv_heads * a.group) + c.head * a.group + hh;
+    const float up = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row_at * DIM + d) =
+        uint2{Half<BF16>::round2(v[0] * up, v[1] * up), Half<BF16>::round2(v[2] * up, v[3] * up)};
+    if (d == 0 && a.lse) a.lse[row_at] = l == 0.f ? -__builtin_inff() : (__builtin_amdgcn_logf(l) + mx) * kLn2;
   }
-  const float own = mx;
-#pragma unroll
-  for (int o = kLanes; o < 64; o <<= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
-  const float down = __builtin_amdgcn_exp2f(own - mx);
-  l *= down;
-  v *= down;
-#pragma unroll
-  for (int o = kLanes; o < 64; o <<= 1) {
-    l += __shfl_xor(l, o);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] += __shfl_xor(v[e], o);
-  }
-  if (gr != 0) return;
-  const int qi = (rt.row0 + r) / a.group, hh = rt.row0 + r - qi * a.group;
-  const int64_t row_at = static_cast<int64_t>(rt.qs + qi) * (a.kv_heads * a.group) + head * a.group + hh;
-  const float up = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row_at * DIM + d) =
-      uint2{Half<BF16>::round2(v[0] * up, v[1] * up), Half<BF16>::round2(v[2] * up, v[3] * up)};
-  if (d == 0 && a.lse) a.lse[row_at] = l == 0.f ? -__builtin_inff() : (__builtin_amdgcn_logf(l) + mx) * kLn2;
 }
 
 template <int DIM, bool BF16>
 hipError_t launch_as(const ChunkParams& a, hipStream_t stream) {
-  const uint32_t units = static_cast<uint32_t>(a.tiles) * a.kv_heads;
-  kv4_chunk_kernel<DIM, BF16><<<dim3(units * a.splits), dim3(kThreads), 0, stream>>>(a);
+  const uint32_t grid = a.groups ? a.groups : static_cast<uint32_t>(a.tiles) * a.kv_heads;
+  kv4_chunk_kernel<DIM, BF16><<<dim3(grid), dim3(kThreads), 0, stream>>>(a);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.splits == 1) return e;
-  kv4_chunk_join_kernel<DIM, BF16><<<dim3(units * (kRows / kJoinWaves)), dim3(kJoinWaves * 64), 0, stream>>>(a);
+  if (e != hipSuccess || a.groups == 0) return e;
+  kv4_chunk_join_kernel<DIM, BF16><<<dim3(static_cast<uint32_t>(a.groups)), dim3(kJoinWaves * 64), 0, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -629,9 +777,10 @@ hipError_t launch_kv4_chunk(const qpn_kv4_cache& c, const qpn_kv4_chunk_args& x,
   a.batch = x.batch, a.rows = x.rows, a.max_q = x.max_q_len < x.rows ? x.max_q_len : x.rows;
   constexpr int kMost = (1 << 30) + (1 << 21);  // no position is above 2^30 + 2^20, and one less this stays inside 32 bits
   a.max_kv = x.max_kv_len, a.window = x.window < kMost ? x.window : kMost;
-  a.tiles = p.tiles, a.splits = p.splits;
+  a.tiles = p.tiles, a.groups = p.groups;
   a.f = x.scale * kLog2e, a.k_scale = c.k_scale, a.v_scale = c.v_scale;
-  a.part = static_cast<float*>(workspace);
+  a.cuts = static_cast<Cut*>(workspace);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.cut_bytes);
   return x.dtype == QPN_DT_BF16 ? launch_dim<true>(c.head_dim, a, stream) : launch_dim<false>(c.head_dim, a, stream);
 }
 

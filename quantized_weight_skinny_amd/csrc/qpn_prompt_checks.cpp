@@ -113,19 +113,20 @@ qpn_status plan_chunk(const qpn_kv4_cache* c, const qpn_kv4_chunk_args* a, Chunk
   // positions and token counts stay inside 32 bits with a step to spare
   if (a->max_kv_len < 0 || a->max_kv_len > (1 << 30) || a->window < 0) return QPN_ERR_INVALID_ARG;
   *p = ChunkPlan{};
-  p->splits = 1;
   if (a->batch == 0 || a->rows == 0) return QPN_OK;
   const int64_t group = a->heads / c->kv_heads, longest = std::min(a->max_q_len, a->rows);
-  // a row of a sequence is counted in 32 bits
+  // a sequence's rows are counted in 32 bits, its cost in sixteenths of a step
   if (longest * group > (1 << 30)) return QPN_ERR_UNSUPPORTED;
   const int64_t tiles = std::min(a->batch * ceil_div(longest * group, kChunkRows), a->rows * group / kChunkRows + a->batch);
   const int64_t units = tiles * c->kv_heads;
-  if (units * (kChunkRows / 4) > kMaxGroups) return QPN_ERR_UNSUPPORTED;
+  if (units > kMaxGroups) return QPN_ERR_UNSUPPORTED;
   p->tiles = static_cast<int>(tiles);
   const int64_t steps = ceil_div(a->max_kv_len, kChunkTokens) + ceil_div(longest, kChunkTokens);
-  if (units < 512) p->splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(512 / units, steps / 4)));
-  if (p->splits > 1)
-    p->total_bytes = static_cast<size_t>(units) * p->splits * kChunkRows * (c->head_dim + 2) * sizeof(float);
+  const int64_t room = kComputeUnits * chunk_groups_per_unit(c->head_dim);
+  // a few steps are over before a join is; and shares are not cut below four steps each
+  if (steps > 8) p->groups = static_cast<int>(std::min<int64_t>(room, ceil_div(units * ceil_div(steps, 4), 8) * 8));
+  p->cut_bytes = static_cast<size_t>(p->groups) * 32;
+  p->total_bytes = p->cut_bytes + static_cast<size_t>(p->groups) * 2 * kChunkRows * (c->head_dim + 2) * sizeof(float);
   return QPN_OK;
 }
 

@@ -30,11 +30,14 @@ qpn_status check_fp8_block_gemm(const qpn_fp8_block_gemm_args* a, const void* ws
 constexpr int kChunkRows = 128;   // query rows (tokens x heads of a group) of a workgroup
 constexpr int kChunkTokens = 64;  // tokens it takes at a time
 
+// Workgroups of the attention kernel that a compute unit holds.
+constexpr int chunk_groups_per_unit(int dim) { return dim == 256 ? 1 : 2; }
+
 // The shape of a chunk attention.
 struct ChunkPlan {
   int tiles;   // row tiles of all sequences, at most
-  int splits;  // shares of a tile's tokens, a workgroup each; 1: no join
-  size_t total_bytes;
+  int groups;  // workgroups that share the work evenly, a multiple of 8; 0: a workgroup a row tile and kv head, no join
+  size_t cut_bytes, total_bytes;
 };
 
 qpn_status plan_chunk(const qpn_kv4_cache* c, const qpn_kv4_chunk_args* a, ChunkPlan* p);

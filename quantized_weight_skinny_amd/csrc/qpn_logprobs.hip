@@ -15,7 +15,7 @@
 // top-th largest of the lanes' maxima over the first 2048 elements: some
 // (vocabulary / 8192) * top candidates follow for one wavefront of a row of no
 // order, and the list is cut back to `top` (by a search over the keys' bits,
-// with votes) when it passes 128, which raises the bound. Rising rows, whose
+// with votes) when it passes twice that, which raises the bound. Rising rows, whose
 // every element passes, cost more and are no less right.
 #include "qpn_decode_internal.hpp"
 #include "qpn_device.hpp"
@@ -27,6 +27,7 @@ namespace {
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kEach = kLogprobsStep / kThreads;  // elements a lane takes at a time
 constexpr int kList = 128;               // candidates that a wavefront keeps
+constexpr int kShort = 80;               // ... and those that a cut leaves
 constexpr int kAtOnce = 8 * 64;          // ... and what it may add before it looks
 constexpr int kKeys = (kList + kAtOnce) / 64;
 typedef u4 u4_anywhere __attribute__((aligned(2)));
@@ -56,17 +57,18 @@ __device__ __forceinline__ float widen(T x) {
   else return static_cast<float>(x);
 }
 
-// A lane's 16 bytes of elements as fp32.
+// A lane's 16 bytes of elements as fp32. (Made quiet once here: a maximum of a
+// signalling NaN would be NaN, and the compiler quiets each operand it does not know.)
 template <typename T>
 __device__ __forceinline__ void widen_piece(const u4& w, float* x) {
   if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(w[e]);
+    for (int e = 0; e < 4; ++e) x[e] = __builtin_canonicalizef(__uint_as_float(w[e]));
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      x[2 * e] = widen16<__is_same(T, Bf16)>(w[e] & 0xFFFFu);
-      x[2 * e + 1] = widen16<__is_same(T, Bf16)>(w[e] >> 16);
+      x[2 * e] = __builtin_canonicalizef(widen16<__is_same(T, Bf16)>(w[e] & 0xFFFFu));
+      x[2 * e + 1] = __builtin_canonicalizef(widen16<__is_same(T, Bf16)>(w[e] >> 16));
     }
   }
 }
@@ -84,40 +86,38 @@ __device__ __forceinline__ uint64_t key_of(float x, int index) {
 }
 constexpr uint32_t kMinusInf = 0x007FFFFFu;  // order_of(-inf)
 
-// Cuts a wavefront's list of n keys (all different) back to the `top` largest,
-// top <= n; returns the order of the smallest that stays.
+// Cuts a wavefront's list of n keys (all different, 0: none; 64 KEYS at most) back to the `top` largest, or
+// some more, kShort at most; top <= n. Returns the order of a bound that at least `top`
+// of them reach and all that stay. The bound is found bit by bit from above: 16
+// bits of the logits' order tell most lists apart, the index those of equal logits.
+template <int KEYS>
 __device__ __forceinline__ uint32_t cut_list(uint64_t* list, int& n, int top) {
   const int lane = threadIdx.x & 63;
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // the list holds other lanes' keys
-  uint64_t key[kKeys];
+  uint64_t key[KEYS];
 #pragma unroll
-  for (int j = 0; j < kKeys; ++j) key[j] = j * 64 + lane < n ? list[j * 64 + lane] : 0;
-  // the largest bound that `top` keys reach, in the upper half, then in the lower among its equals
-  uint64_t bound = 0;
-#pragma unroll 1
-  for (int bit = 63; bit >= 32; --bit) {
-    const uint64_t next = bound | uint64_t(1) << bit;
+  for (int j = 0; j < KEYS; ++j) key[j] = j * 64 + lane < n ? list[j * 64 + lane] : 0;
+  const auto reach = [&](uint64_t x) {
     int count = 0;
 #pragma unroll
-    for (int j = 0; j < kKeys; ++j) count += __popcll(__ballot(static_cast<uint32_t>(key[j] >> 32) >= static_cast<uint32_t>(next >> 32)));
-    if (count >= top) bound = next;
-  }
-  int reach = 0;
-#pragma unroll
-  for (int j = 0; j < kKeys; ++j) reach += __popcll(__ballot(key[j] >= bound));
-  if (reach > top) {
-#pragma unroll 1
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint64_t next = bound | uint64_t(1) << bit;
-      int count = 0;
-#pragma unroll
-      for (int j = 0; j < kKeys; ++j) count += __popcll(__ballot(key[j] >= next));
-      if (count >= top) bound = next;
+    for (int j = 0; j < KEYS; ++j) {
+      if (j * 64 >= n) break;
+      count += __popcll(__ballot(key[j] >= x));
     }
+    return count;
+  };
+  uint64_t bound = 0;
+#pragma unroll 1
+  for (int bit = 63; bit >= 0; --bit) {
+    const uint64_t next = bound | uint64_t(1) << bit;
+    if (reach(next) >= top) bound = next;
+    if ((bit & 15) == 0 && reach(bound) <= kShort) break;
   }
+  bound = max(bound, uint64_t(1));  // (places without a key go, too)
   int at = 0;
 #pragma unroll
-  for (int j = 0; j < kKeys; ++j) {
+  for (int j = 0; j < KEYS; ++j) {
+    if (j * 64 >= n) break;
     const uint64_t stays = __ballot(key[j] >= bound);
     const int mine = at + __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(stays >> 32),
                                                     __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(stays), 0));
@@ -203,6 +203,21 @@ __global__ __launch_bounds__(kThreads) void logprobs_slices_kernel(const Logprob
   const int row = blockIdx.x / p.slices, slice = blockIdx.x - row * p.slices;
   const T* x0 = static_cast<const T*>(p.a.logits) + row * p.a.row_stride;
   const int begin = slice * p.length, end = min(begin + p.length, p.a.vocab);
+  u4 raw[kPieces];
+  constexpr int kWaveStep = kEach * 64;
+  const auto load = [&](int at) {
+    const T* from = x0 + at + lane * kPiece;
+    if (at + kWaveStep <= end) {
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) raw[j] = *reinterpret_cast<const u4_anywhere*>(from + j * 64 * kPiece);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j)
+        if (at + (j * 64 + lane + 1) * kPiece <= end) raw[j] = *reinterpret_cast<const u4_anywhere*>(from + j * 64 * kPiece);
+    }
+  };
+  const int at0 = begin + wave * kWaveStep;
+  if (at0 < end) load(at0);
   const float f = factor_of(p, row);
   const int token = p.a.tokens ? p.a.tokens[row] : -1;
   const bool given = token >= 0 && token < p.a.vocab;
@@ -220,18 +235,9 @@ __global__ __launch_bounds__(kThreads) void logprobs_slices_kernel(const Logprob
   float bound = -__builtin_inff();
   bool first = true;
   uint64_t* list = lists[TOP ? wave : 0];
+  // (a short list is cut by a hundred instructions, and a bound that rises early spares most steps)
+  const int enough = min(2 * p.a.top + 8, kList);
 
-  u4 raw[kPieces];
-  const auto load = [&](int at) {
-#pragma unroll
-    for (int j = 0; j < kPieces; ++j) {
-      const int e0 = at + j * 64 * kPiece + lane * kPiece;
-      if (e0 + kPiece <= end) raw[j] = *reinterpret_cast<const u4_anywhere*>(x0 + e0);
-    }
-  };
-  constexpr int kWaveStep = kEach * 64;
-  const int at0 = begin + wave * kWaveStep;
-  if (at0 < end) load(at0);
   for (int at = at0; at < end; at += kWaveStep * kWaves) {
     float x[kEach];
 #pragma unroll
@@ -248,9 +254,10 @@ __global__ __launch_bounds__(kThreads) void logprobs_slices_kernel(const Logprob
       }
     }
     if (at + kWaveStep * kWaves < end) load(at + kWaveStep * kWaves);
-    float top = m;
+    float most = x[0];
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) top = fmaxf(top, x[e]);
+    for (int e = 1; e < kEach; ++e) most = fmaxf(most, x[e]);
+    const float top = fmaxf(m, most);
     if (__any(top > m)) {
       move_reference(s, w, (m - top) * f);
       m = top;
@@ -265,17 +272,15 @@ __global__ __launch_bounds__(kThreads) void logprobs_slices_kernel(const Logprob
       s += y;
       w = fmaf(y, t, w);
     }
+    // (for a likely token, most steps hold none that comes before it)
     if (mixed) {
 #pragma unroll
       for (int e = 0; e < kEach; ++e) before += x[e] >= (index(e) >= token ? above : reach);
-    } else {
+    } else if (__any(most >= least)) {
 #pragma unroll
       for (int e = 0; e < kEach; ++e) before += x[e] >= least;
     }
     if constexpr (TOP) {
-      float most = x[0];
-#pragma unroll
-      for (int e = 1; e < kEach; ++e) most = fmaxf(most, x[e]);
       bool equal = false;  // elements that equal the bound count
       if (first) {
         // the upper 16 bits of the top-th largest of the lanes' maxima
@@ -290,13 +295,10 @@ __global__ __launch_bounds__(kThreads) void logprobs_slices_kernel(const Logprob
         first = false;
       }
       if (__any(equal ? most >= bound : most > bound)) {
-#pragma unroll 1
+#pragma unroll
         for (int part = 0; part < kEach / 8; ++part) {
           // (the eight elements of a part lie in front of the next part's for all lanes)
-          float y[8];
-#pragma unroll
-          for (int e = 0; e < kEach; ++e)
-            if (e / 8 == part) y[e % 8] = x[e];
+          const float* y = &x[part * 8];
           float z = y[0];
 #pragma unroll
           for (int e = 1; e < 8; ++e) z = fmaxf(z, y[e]);
@@ -306,8 +308,8 @@ __global__ __launch_bounds__(kThreads) void logprobs_slices_kernel(const Logprob
             const bool take = equal ? y[e] >= bound : y[e] > bound;
             if (__any(take)) add_keys(list, n, take, key_of(y[e], index(part * 8 + e)));
           }
-          if (n > kList) {
-            bound = value_of(cut_list(list, n, p.a.top));
+          if (n > enough) {
+            bound = value_of(cut_list<kKeys>(list, n, p.a.top));
             equal = false;
           }
         }
@@ -349,14 +351,18 @@ __global__ __launch_bounds__(kThreads) void logprobs_slices_kernel(const Logprob
 // A row's slices as one, and its results.
 template <typename T, bool TOP>
 __global__ __launch_bounds__(kThreads) void logprobs_rows_kernel(const LogprobsParams p) {
-  __shared__ uint64_t lists[TOP ? kWaves : 1][kList + kAtOnce];
-  __shared__ int counts[kWaves], infinite;
-  __shared__ uint64_t first[TOP ? 64 : 1];
+  __shared__ uint64_t keys[TOP ? kLogprobsKeys : 1], first[TOP ? 64 : 1];
+  __shared__ int infinite, found, left;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   const int row = blockIdx.x;
   const T* x0 = static_cast<const T*>(p.a.logits) + row * p.a.row_stride;
+  // (asked for early: each of these waits for the one before)
+  const int token = p.a.tokens ? p.a.tokens[row] : -1;
+  const float given_t = p.a.temperature ? p.a.temperature[row] : 1.0f;
+  const bool given = token >= 0 && token < p.a.vocab;
+  const float given_x = given ? widen<T>(x0[token]) : 0.f;
   const float f = factor_of(p, row);
-  if (threadIdx.x == 0) infinite = 0;
+  if (threadIdx.x == 0) infinite = 0, found = 0;
   // every wavefront adds all slices
   Stat r{0.0, 0.0, kLowest, 0};
   for (int c = lane; c < p.slices; c += 64) {
@@ -371,17 +377,10 @@ __global__ __launch_bounds__(kThreads) void logprobs_rows_kernel(const LogprobsP
   r.sum = wave_add(r.sum), r.dot = wave_add(r.dot), r.max = most;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) r.before += __shfl_xor(r.before, o);
+  const int total = p.slices * p.a.top;
   if constexpr (TOP) {
-    const uint64_t* in = p.lists + static_cast<int64_t>(row) * p.slices * p.a.top;
-    const int total = p.slices * p.a.top;
-    int n = 0;
-    uint64_t bound = 0;
-    for (int j0 = wave * 64; j0 < total; j0 += kThreads) {
-      const uint64_t key = j0 + lane < total ? in[j0 + lane] : 0;
-      if (__any(key > bound)) add_keys(lists[wave], n, key > bound, key);
-      if (n > kList) bound = static_cast<uint64_t>(cut_list(lists[wave], n, p.a.top)) << 32;
-    }
-    if (lane == 0) counts[wave] = n;
+    const uint64_t* in = p.lists + static_cast<int64_t>(row) * total;
+    for (int j = threadIdx.x; j < total; j += kThreads) keys[j] = in[j];
   }
   __syncthreads();
   if (r.max == __builtin_inff()) {
@@ -393,7 +392,6 @@ __global__ __launch_bounds__(kThreads) void logprobs_rows_kernel(const LogprobsP
     r.sum = infinite, r.dot = 0.0;
   }
   // log p = ((x - max) / t) - ln s
-  const float given_t = p.a.temperature ? p.a.temperature[row] : 1.0f;
   const double t = given_t > 0.f ? given_t : 1.0f, log_sum = r.sum > 0.0 ? log(r.sum) : 0.0;
   const auto log_p = [&](float x) -> float {
     if (!(x > -__builtin_inff())) return -__builtin_inff();
@@ -401,16 +399,30 @@ __global__ __launch_bounds__(kThreads) void logprobs_rows_kernel(const LogprobsP
     return static_cast<float>((static_cast<double>(x) - static_cast<double>(r.max)) / t - log_sum);
   };
   if (threadIdx.x == 0) {
-    const int token = p.a.tokens ? p.a.tokens[row] : -1;
-    const bool given = token >= 0 && token < p.a.vocab;
-    const float x = given ? widen<T>(x0[token]) : 0.f;
-    if (p.a.logprobs) p.a.logprobs[row] = given ? log_p(x) : 0.f;
+    if (p.a.logprobs) p.a.logprobs[row] = given ? log_p(given_x) : 0.f;
     // (all in front of a logit of -inf or NaN come before it)
-    if (p.a.rank) p.a.rank[row] = given ? r.before + (x > -__builtin_inff() ? 0 : token) : -1;
+    if (p.a.rank) p.a.rank[row] = given ? r.before + (given_x > -__builtin_inff() ? 0 : token) : -1;
     if (p.a.entropy) p.a.entropy[row] = r.sum > 0.0 ? static_cast<float>(fmax(log_sum - r.dot / r.sum * 0.69314718055994530942, 0.0)) : 0.f;
   }
   if constexpr (TOP) {
-    const int found = merge_lists(lists, counts, p.a.top, [&](uint64_t key, int place) { first[place] = key; });
+    // the first `top` of all slices', or some more
+    if (wave == 0) {
+      int n = total;
+      if (p.slices > 1) cut_list<kLogprobsKeys / 64>(keys, n, p.a.top);
+      if (lane == 0) left = n;
+    }
+    __syncthreads();
+    for (int j = threadIdx.x; j < left; j += kThreads) {
+      const uint64_t key = keys[j];
+      int place = 0;
+#pragma unroll 8
+      for (int i = 0; i < left; ++i) place += keys[i] > key;
+      if (key != 0 && place < p.a.top) {
+        first[place] = key;
+        atomicAdd(&found, 1);
+      }
+    }
+    __syncthreads();
     // fewer tokens than asked for are above -inf: the others in the order of their index
     if (found < p.a.top && wave == 0) {
       int n = found;

@@ -165,7 +165,7 @@ bool plan_logprobs(int32_t rows, int32_t vocab, int32_t top, LogprobsPlan* p) {
   *p = LogprobsPlan{};
   // as many slices as bring 2048 workgroups, 8 for each compute unit
   const int64_t wanted = rows > 0 ? ceil_div(2048, rows) : 1;
-  const int64_t most = std::min<int64_t>(ceil_div(vocab, kLogprobsStep), kLogprobsSlices);
+  const int64_t most = std::min<int64_t>(ceil_div(vocab, kLogprobsStep), top > 0 ? std::min(kLogprobsSlices, kLogprobsKeys / top) : kLogprobsSlices);
   const int64_t length = ceil_div(ceil_div(vocab, std::min(wanted, most)), kLogprobsStep) * kLogprobsStep;
   p->length = static_cast<int>(length);
   p->slices = static_cast<int>(ceil_div(vocab, length));

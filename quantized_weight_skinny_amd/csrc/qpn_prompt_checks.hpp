@@ -44,7 +44,8 @@ qpn_status plan_chunk(const qpn_kv4_cache* c, const qpn_kv4_chunk_args* a, Chunk
 qpn_status check_kv4_chunk(const qpn_kv4_cache* c, const qpn_kv4_chunk_args* a, const void* ws, size_t ws_bytes,
                            ChunkPlan* p, bool* run);
 
-constexpr int kLogprobsStep = 8192;   // elements of a row that a workgroup takes at a time
+constexpr int kLogprobsStep = 4096;   // elements of a row that a workgroup takes at a time
+constexpr int kLogprobsKeys = 2048;   // first tokens of a row's slices, at most
 constexpr int kLogprobsSlices = 128;  // slices of a row, at most
 
 // The shape of token log-probabilities: every row in `slices` of `length`.

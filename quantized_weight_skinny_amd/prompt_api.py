@@ -32,6 +32,7 @@ from .prompt import (
 
 BLOCK = 128  # elements under one scale
 CODES = (torch.uint8, torch.float8_e4m3fn)
+FLOATS = tuple(DTYPES)
 
 
 def _blocks(n):
@@ -44,12 +45,14 @@ def _matrix(t, name, device, dtypes, shape=None):
     _on_device(t, name, device)
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be one of {', '.join(str(d) for d in dtypes)}, not {t.dtype}")
-    if t.dim() != 2 or (shape is not None and t.shape != shape):
-        raise ValueError(f"{name} must have shape {shape or ('rows', 'columns')}, not {tuple(t.shape)}")
-    rows, columns = t.shape
-    if columns > 1 and t.stride(1) != 1 and t.numel():
+    sizes = t.shape
+    if len(sizes) != 2 or (shape is not None and sizes != shape):
+        raise ValueError(f"{name} must have shape {shape or ('rows', 'columns')}, not {tuple(sizes)}")
+    rows, columns = sizes
+    stride, step = t.stride()
+    if step != 1 and columns > 1 and rows:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    return t.data_ptr(), t.stride(0) if rows > 1 and columns > 0 else columns
+    return t.data_ptr(), stride if rows > 1 and columns > 0 else columns
 
 
 def _block_scales(t, shape, name, device):
@@ -62,7 +65,7 @@ def _block_scales(t, shape, name, device):
 
 def _quantize(x, block_rows, codes, scales):
     dev = x.device if isinstance(x, torch.Tensor) else None
-    xp, stride = _matrix(x, "x", dev, tuple(DTYPES))
+    xp, stride = _matrix(x, "x", dev, FLOATS)
     rows, k = x.shape
     if codes is None:
         codes = torch.empty((rows, -(-k // 16) * 16), dtype=torch.float8_e4m3fn, device=dev)[:, :k]
@@ -132,7 +135,7 @@ def _product(x, scales, w, dtype, out, workspace):
     dev = w.device
     n, k = w.n, w.k
     coded = scales is not None
-    xp, x_stride = _matrix(x, "codes" if coded else "x", dev, CODES if coded else tuple(DTYPES))
+    xp, x_stride = _matrix(x, "codes" if coded else "x", dev, CODES if coded else FLOATS)
     m = x.shape[0]
     if x.shape[1] != k:
         raise ValueError(f"{'codes' if coded else 'x'} must have shape (rows, {k}), not {tuple(x.shape)}")
@@ -279,11 +282,11 @@ def token_logprobs(logits, tokens, top=0, temperature=None, logprobs=None, entro
     p, how many tokens come before the given one (-1), and the first `top` (0
     to 64) tokens. Larger logits come first, equal ones in the order of their
     index; NaN counts as -inf."""
-    _on_device(logits, "logits")
+    xp, stride = _matrix(logits, "logits", None, FLOATS)
     dev = logits.device
-    xp, stride = _matrix(logits, "logits", dev, tuple(DTYPES))
     rows, vocab = logits.shape
-    _sizes(rows=rows, vocab=vocab, top=top)
+    if not (0 <= top <= INT32_MAX and rows <= INT32_MAX and vocab <= INT32_MAX):
+        raise ValueError(f"{rows} rows, a vocabulary of {vocab} and top {top} must be 0 .. {INT32_MAX}")
     tp = _exactly(tokens, torch.int32, (rows,), "tokens", dev)
     fp = None if temperature is None else _exactly(temperature, torch.float32, (rows,), "temperature", dev)
     logprobs = _out(logprobs, torch.float32, (rows,), "logprobs", dev)

@@ -18,6 +18,8 @@
 // fp16 or bf16, and too much for an fp32 result: there the codes are brought
 // to fp16, which holds them exactly, for v_mfma_f32_16x16x32_f16, whose sums are
 // fp32 (EXACT below), at half the rate.
+#include <algorithm>
+
 #include "qpn_decode_internal.hpp"
 #include "qpn_device.hpp"
 #include "qpn_prompt_internal.hpp"
@@ -164,8 +166,8 @@ struct ProductParams {
   void* y;
   float* partial;  // [splits][m][n] where splits > 1
   int64_t x_stride, xs_row, xs_block, w_stride, ws_row, ws_block, y_stride;
-  int64_t m, n;
-  int32_t k, blocks, splits, y_dtype, y_vec;
+  int64_t m, n, n_first;  // (many rows: the tiles' first output)
+  int32_t k, blocks, splits, tiles, y_dtype, y_vec;
 };
 
 // 32 codes of one row: a lane's part of a block, as fp16 where EXACT.
@@ -300,103 +302,154 @@ __device__ __forceinline__ void lds_dma(const uint8_t* base, uint32_t offset, ui
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %2" ::"v"(offset), "s"(dst), "s"(base)
                : "memory", "m0");
 }
+// The same of 4 bytes a lane.
+__device__ __forceinline__ void lds_dma4(const float* base, uint32_t offset, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, %2" ::"v"(offset), "s"(dst), "s"(base)
+               : "memory", "m0");
+}
 #pragma clang diagnostic pop
+
+typedef const float __attribute__((address_space(4))) * scalar_ptr;  // read through the scalar cache
 
 // Many rows: MW x NW wavefronts of TM x TN tiles of 16 x 16 each. Both
 // operands' 128 bytes of a block go to LDS, the next block's while this one is
 // multiplied. A row's eight 16-byte pieces lie in LDS at piece ^ (row % 8), so
 // that neighbouring rows' reads meet different banks.
+//
+// Within a block the products of one row tile are issued while the sums of the
+// one before are scaled, and the next one's codes are on their way: a result
+// that is used at once costs the pipeline's depth, 12 cycles of 44. At 256 x 256
+// that takes all registers: the last tile of rows begins early enough to be
+// whole (its rows are computed twice, to the same bits), and one offset serves
+// all of a thread's rows of x.
+//
+// Workgroups go round the eight dies. Each die takes an eighth of the tiles, row
+// tiles first: its 32 compute units read 8 x 4 tiles' rows between them rather
+// than 1 x 32, from a cache that holds a fraction of either operand.
 template <int MW, int NW, int TM, int TN, bool EXACT>
 __global__ __launch_bounds__(MW * NW * 64, 2) void many_rows_kernel(const ProductParams p) {
   constexpr int kThreads = MW * NW * 64, kM = MW * TM * 16, kN = NW * TN * 16;
-  constexpr int kStage = (kM + kN) * kScaleBlock, kLoads = kStage / 16 / kThreads;
-  static_assert(kStage % (16 * kThreads) == 0 && kM * 8 % kThreads == 0, "whole loads of either operand");
+  constexpr bool kWhole = kM == 256;  // every tile's rows are there
+  constexpr int kStage = (kM + kN) * kScaleBlock, kRowsAtOnce = kThreads / 8;
+  constexpr int kLoadsX = kM / kRowsAtOnce, kLoadsW = kN / kRowsAtOnce;
+  static_assert(kM % kRowsAtOnce == 0 && kN % kRowsAtOnce == 0 && kRowsAtOnce % 8 == 0, "whole loads of either operand");
   static_assert(kScaleBlock % (TN * 16) == 0, "a wavefront's outputs share their scale");
   __shared__ alignas(16) uint8_t lds[2][kStage];  // x rows, then w rows
+  __shared__ alignas(16) float scales[2][kM];     // of x: a wavefront's rows t * 16 + i at i * TM + t
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i = lane & 15, g = lane >> 4;
-  const int64_t m_tiles = (p.m + kM - 1) / kM;
-  const int64_t m0 = blockIdx.x % m_tiles * kM, n0 = blockIdx.x / m_tiles * kN;
+  const int m_tiles = static_cast<int>((p.m + kM - 1) / kM);
+  const int per_die = (gridDim.x + 7) / 8, tile = blockIdx.x % 8 * per_die + blockIdx.x / 8;
+  if (tile >= p.tiles) return;  // (the grid is a multiple of 8)
+  const int64_t m_first = static_cast<int64_t>(tile % m_tiles) * kM;
+  const int64_t m0 = kWhole ? min(m_first, p.m - kM) : m_first, n0 = p.n_first + tile / m_tiles * static_cast<int64_t>(kN);
   const int wm = wave % MW, wn = wave / MW;
   const int split = blockIdx.y;
   const int b0 = static_cast<int>(static_cast<int64_t>(p.blocks) * split / p.splits);
   const int b1 = static_cast<int>(static_cast<int64_t>(p.blocks) * (split + 1) / p.splits);
   const uint8_t* x = p.x + m0 * p.x_stride;
   const uint8_t* w = p.w + n0 * p.w_stride;
-  // the rows and pieces that this thread brings: piece `tid` of every kThreads
-  uint32_t from[kLoads];
+  // the rows and pieces that this thread brings: row tid / 8 of every kRowsAtOnce
+  const uint32_t piece = ((tid & 7) ^ (tid >> 3 & 7)) * 16;
+  uint32_t from_x[kWhole ? 1 : kLoadsX], from_w[kLoadsW];
 #pragma unroll
-  for (int j = 0; j < kLoads; ++j) {
-    const int piece = j * kThreads + tid, row = piece / 8, c = (piece & 7) ^ (row & 7);
-    const bool of_x = j * kThreads < kM * 8;
-    const int64_t last = (of_x ? p.m - 1 - m0 : p.n - 1 - n0), r = of_x ? row : row - kM;
-    from[j] = static_cast<uint32_t>((r < last ? r : last) * (of_x ? p.x_stride : p.w_stride)) + c * 16;
-  }
-  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_void)(&lds[0][0])));
-  const auto load = [&](int b, int buf) {
-    const int at = b * kScaleBlock;
-    if (at + kScaleBlock <= p.k) {
+  for (int j = 0; j < (kWhole ? 1 : kLoadsX); ++j)
+    from_x[j] = static_cast<uint32_t>(min(static_cast<int64_t>(j * kRowsAtOnce + tid / 8), p.m - 1 - m0) * p.x_stride) + piece;
 #pragma unroll
-      for (int j = 0; j < kLoads; ++j)
-        lds_dma((j * kThreads < kM * 8 ? x : w) + at, from[j],
-                __builtin_amdgcn_readfirstlane(lds0 + buf * kStage + j * kThreads * 16 + wave * 1024));
-    } else {
-      // the short last block: pieces past the end of k are zeros
+  for (int j = 0; j < kLoadsW; ++j)
+    from_w[j] = static_cast<uint32_t>(min(static_cast<int64_t>(j * kRowsAtOnce + tid / 8), p.n - 1 - n0) * p.w_stride) + piece;
+  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_void)(&lds[0][0]))) + wave * 1024;
+  const auto x_rows = [&](int b, int j) {
+    return x + static_cast<int64_t>(b) * kScaleBlock + (kWhole ? j * kRowsAtOnce * p.x_stride : 0);
+  };
+  // Load j of this wavefront's of a whole block.
+  const auto bring = [&](int b, int buf, int j) {
+    const uint32_t to = __builtin_amdgcn_readfirstlane(lds0 + buf * kStage + j * kThreads * 16);
+    if (j < kLoadsX) lds_dma(x_rows(b, j), from_x[kWhole ? 0 : j], to);
+    else lds_dma(w + static_cast<int64_t>(b) * kScaleBlock, from_w[j - kLoadsX], to);
+  };
+  // The short last block: pieces past the end of k are zeros.
+  const auto bring_short = [&](int b, int buf) {
+    const bool in = b * kScaleBlock + static_cast<int>(piece) < p.k;
 #pragma unroll
-      for (int j = 0; j < kLoads; ++j) {
-        const int piece = j * kThreads + tid, c = (piece & 7) ^ (piece / 8 & 7);
-        u4 v = {0u, 0u, 0u, 0u};
-        if (at + c * 16 < p.k) v = *reinterpret_cast<const u4*>((j * kThreads < kM * 8 ? x : w) + at + from[j]);
-        *reinterpret_cast<u4*>(&lds[buf][piece * 16]) = v;
-      }
+    for (int j = 0; j < kLoadsX + kLoadsW; ++j) {
+      const uint8_t* from = j < kLoadsX ? x_rows(b, j) + from_x[kWhole ? 0 : j]
+                                        : w + static_cast<int64_t>(b) * kScaleBlock + from_w[j < kLoadsX ? 0 : j - kLoadsX];
+      u4 v = {0u, 0u, 0u, 0u};
+      if (in) v = *reinterpret_cast<const u4*>(from);
+      *reinterpret_cast<u4*>(&lds[buf][(j * kThreads + tid) * 16]) = v;
     }
   };
-  const float* ws = p.ws + (n0 + wn * TN * 16 < p.n ? (n0 + wn * TN * 16) / kScaleBlock : 0) * p.ws_row;
-  const float* xs = p.xs + m0 * p.xs_row;
-  uint32_t xs_row[TM];
-#pragma unroll
-  for (int t = 0; t < TM; ++t)
-    xs_row[t] = static_cast<uint32_t>(min(static_cast<int64_t>((wm * TM + t) * 16 + i), p.m - 1 - m0) * p.xs_row);
-  float sw, sx[TM];
-  const auto load_scales = [&](int b) {
-    sw = ws[b * p.ws_block];
-#pragma unroll
-    for (int t = 0; t < TM; ++t) sx[t] = (xs + b * p.xs_block)[xs_row[t]];
+  // x's scales: 64 rows a wavefront's, by the first kM / 64 of them.
+  const uint32_t scale_slot = wave * 64 + lane, scale_part = scale_slot / (TM * 16), in_part = scale_slot % (TM * 16);
+  const uint32_t from_s = static_cast<uint32_t>(
+      min(static_cast<int64_t>(scale_part * (TM * 16) + in_part % TM * 16 + in_part / TM), p.m - 1 - m0) * p.xs_row * 4);
+  const uint32_t scales0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_void)(&scales[0][0]))) + wave * 256;
+  const auto bring_scales = [&](int b, int buf) {
+    if (wave < kM / 64)
+      lds_dma4(p.xs + m0 * p.xs_row + b * p.xs_block, from_s, __builtin_amdgcn_readfirstlane(scales0 + buf * kM * 4));
   };
+  const int64_t w_block = n0 + wn * TN * 16 < p.n ? (n0 + wn * TN * 16) / kScaleBlock : 0;
+  const scalar_ptr ws = (scalar_ptr)(p.ws + w_block * p.ws_row);
   f4 acc[TM][TN];
 #pragma unroll
   for (int t = 0; t < TM; ++t)
 #pragma unroll
     for (int u = 0; u < TN; ++u) acc[t][u] = f4{0.f, 0.f, 0.f, 0.f};
   const int slot0 = ((g ^ (i & 7)) * 16), slot1 = (((g + 4) ^ (i & 7)) * 16);
+  constexpr int kLoads = kLoadsX + kLoadsW;
+  float sw = 0.f;
   if (b0 < b1) {
-    load(b0, 0);
-    load_scales(b0);
+    bring_scales(b0, 0);
+    sw = ws[b0 * p.ws_block];
+    if ((b0 + 1) * kScaleBlock <= p.k) {
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) bring(b0, 0, j);
+    } else {
+      bring_short(b0, 0);
+    }
   }
   for (int b = b0; b < b1; ++b) {
     const int buf = (b - b0) & 1;
-    float s[TM];
     __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
     __syncthreads();
-#pragma unroll
-    for (int t = 0; t < TM; ++t) s[t] = sx[t] * sw;
-    if (b + 1 < b1) {
-      load(b + 1, buf ^ 1);
-      load_scales(b + 1);
-    }
     const uint8_t* xt = &lds[buf][(wm * TM * 16 + i) * kScaleBlock];
     const uint8_t* wt = &lds[buf][(kM + wn * TN * 16 + i) * kScaleBlock];
     const auto frag = [&](const uint8_t* rows) {
       return Frag<EXACT>(*reinterpret_cast<const u4*>(rows + slot0), *reinterpret_cast<const u4*>(rows + slot1));
     };
-    Frag<EXACT> wf[TN];
+    Frag<EXACT> wf[TN], xf[2];
+    xf[0] = frag(xt);
 #pragma unroll
     for (int u = 0; u < TN; ++u) wf[u] = frag(wt + u * 16 * kScaleBlock);
+    f4 s[TM / 4];
 #pragma unroll
-    for (int t = 0; t < TM; ++t) {
-      const Frag<EXACT> xf = frag(xt + t * 16 * kScaleBlock);
+    for (int t = 0; t < TM / 4; ++t) s[t] = *reinterpret_cast<const f4*>(&scales[buf][(wm * 16 + i) * TM + t * 4]) * sw;
+    const bool more = b + 1 < b1, whole = (b + 2) * kScaleBlock <= p.k;
+    if (more) {
+      bring_scales(b + 1, buf ^ 1);
+      sw = ws[(b + 1) * p.ws_block];
+      if (!whole) bring_short(b + 1, buf ^ 1);
+    }
+    f4 sums[2][TN];
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int u = 0; u < TN; ++u) acc[t][u] += block_sums(wf[u], xf) * s[t];
+    for (int t = 0; t <= TM; ++t) {
+      if (t + 1 < TM) xf[(t + 1) & 1] = frag(xt + (t + 1) * 16 * kScaleBlock);
+      // (the next block's loads are spread over the first half of this one: all at once they stand in the way of LDS reads)
+      if (t < TM / 2 && more && whole) {
+#pragma unroll
+        for (int j = kLoads * t / (TM / 2); j < kLoads * (t + 1) / (TM / 2); ++j) bring(b + 1, buf ^ 1, j);
+      }
+#pragma unroll
+      for (int u = 0; u < TN; ++u) {
+        if (t < TM) sums[t & 1][u] = block_sums(wf[u], xf[t & 1]);
+        if (t > 0) {
+          acc[t - 1][u] += sums[(t - 1) & 1][u] * s[(t - 1) / 4][(t - 1) % 4];
+          asm volatile("" : "+v"(acc[t - 1][u]));  // (here: the compiler would gather them behind the loads)
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
   }
 #pragma unroll
@@ -482,7 +535,7 @@ hipError_t launch_fp8_block_quantize(const void* x, int32_t dtype, int64_t rows,
 
 hipError_t launch_fp8_block_gemm(const qpn_fp8_block_gemm_args& a, const Fp8BlockPlan& plan, void* workspace,
                                  hipStream_t stream) {
-  ProductParams p;
+  ProductParams p = {};
   uint8_t* base = static_cast<uint8_t*>(workspace);
   float* own_scales = reinterpret_cast<float*>(base + plan.code_bytes);
   if (a.x_dtype == QPN_DT_E4M3) {
@@ -514,18 +567,25 @@ hipError_t launch_fp8_block_gemm(const qpn_fp8_block_gemm_args& a, const Fp8Bloc
       default: return exact ? launch_few<4, true>(plan.waves, grid, p, stream) : launch_few<4, false>(plan.waves, grid, p, stream);
     }
   }
-  // (two times 4 fp16 fragments and their 32 results beside 128 sums would not fit the registers)
   const bool exact = a.y_dtype == QPN_DT_F32;
-  const int tile = exact ? 128 : plan.tile;
-  const int64_t tiles = (a.m + tile - 1) / tile * ((a.n + tile - 1) / tile);
-  const dim3 grid(static_cast<uint32_t>(tiles), static_cast<uint32_t>(plan.splits));
-  if (exact)
-    many_rows_kernel<2, 2, 4, 4, true><<<grid, dim3(256), 0, stream>>>(p);
-  else if (tile == 256)
-    many_rows_kernel<2, 4, 8, 4, false><<<grid, dim3(512), 0, stream>>>(p);
-  else
-    many_rows_kernel<2, 2, 4, 4, false><<<grid, dim3(256), 0, stream>>>(p);
-  hipError_t e = hipGetLastError();
+  const auto launch = [&](int tile, int64_t first, int64_t last) {
+    p.n_first = first;
+    p.tiles = static_cast<int32_t>((a.m + tile - 1) / tile * ((last - first + tile - 1) / tile));
+    const dim3 grid(static_cast<uint32_t>((p.tiles + 7) / 8 * 8), static_cast<uint32_t>(plan.splits));
+    if (exact)  // (16 fp16 fragments beside 128 sums would not fit the registers)
+      many_rows_kernel<2, 2, 4, 4, true><<<grid, dim3(256), 0, stream>>>(p);
+    else if (tile == 256)
+      many_rows_kernel<2, 4, 8, 4, false><<<grid, dim3(512), 0, stream>>>(p);
+    else
+      many_rows_kernel<2, 2, 4, 4, false><<<grid, dim3(256), 0, stream>>>(p);
+    return hipGetLastError();
+  };
+  if (!exact && plan.wide > 0) {
+    const hipError_t e = launch(256, 0, std::min(plan.wide, a.n));
+    if (e != hipSuccess || plan.wide >= a.n) return e;
+    return launch(128, plan.wide, a.n);
+  }
+  hipError_t e = launch(128, 0, a.n);
   if (e != hipSuccess || plan.splits == 1) return e;
   const int64_t quads = a.m * ((a.n + 3) / 4);
   join_kernel<<<dim3(static_cast<uint32_t>((quads + 255) / 256)), dim3(256), 0, stream>>>(p);

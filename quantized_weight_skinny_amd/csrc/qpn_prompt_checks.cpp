@@ -38,10 +38,17 @@ bool plan_fp8_block(int64_t m, int64_t n, int64_t k, Fp8BlockPlan* p) {
     p->waves = 4;
     while (p->waves < (p->m_tiles == 4 ? 8 : 16) && ceil_div(n, 16) * p->waves < 2048 && p->blocks >= 8 * p->waves) p->waves *= 2;
   } else {
-    p->tile = m > 128 && ceil_div(m, 256) * ceil_div(n, 256) >= 200 ? 256 : 128;
-    const int64_t tiles = ceil_div(m, p->tile) * ceil_div(n, p->tile);
-    // (fp32 results take tiles of 128 always)
-    if (ceil_div(m, 128) * ceil_div(n, 128) > kMaxGroups) return false;
+    // Tiles of 256 x 256, one a compute unit, where they come in whole rounds of 256; the
+    // outputs of the last round that would not be full go in tiles of 128 x 128. (fp32
+    // results take those always.)
+    const int64_t m_tiles = ceil_div(m, 256), n_tiles = ceil_div(n, 256), rounds = m_tiles * n_tiles / kComputeUnits;
+    if (m >= 256 && rounds > 0) {
+      const int64_t left = m_tiles * n_tiles - rounds * kComputeUnits;
+      p->wide = left > kComputeUnits * 3 / 4 ? n : rounds * kComputeUnits / m_tiles * 256;
+      p->wide = std::min(p->wide, n);
+    }
+    const int64_t tiles = ceil_div(m, 128) * ceil_div(n, 128);
+    if (tiles > kMaxGroups) return false;
     if (tiles < 256)
       p->splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(512 / std::max<int64_t>(1, tiles), p->blocks / 8)));
   }

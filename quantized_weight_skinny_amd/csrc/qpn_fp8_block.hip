@@ -28,7 +28,7 @@ namespace qpn {
 namespace {
 
 typedef int i8 __attribute__((ext_vector_type(8)));
-typedef u4 u4_anywhere __attribute__((aligned(2)));
+typedef const float __attribute__((address_space(4))) * scalar_ptr;  // read through the scalar cache
 
 // ------------------------------------------------------------------ quantizer
 
@@ -228,70 +228,6 @@ __device__ __forceinline__ void store4(const ProductParams& p, int64_t row, int6
   }
 }
 
-// Few rows: a workgroup takes 16 outputs, its wavefronts every WAVES-th block
-// of k each, straight from memory into registers; their sums are added in LDS
-// in the order of the wavefronts.
-template <int MT, int WAVES, bool EXACT>
-__global__ __launch_bounds__(WAVES * 64) void few_rows_kernel(const ProductParams p) {
-  __shared__ f4 red[WAVES][MT][64];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
-  const int i = lane & 15, g = lane >> 4;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
-  const uint8_t* w = p.w + n0 * p.w_stride;
-  const int w_row = static_cast<int>(min(static_cast<int64_t>(i), p.n - 1 - n0) * p.w_stride) + g * 16;
-  const float* ws = p.ws + n0 / kScaleBlock * p.ws_row;
-  int64_t x_row[MT];
-  const float* xs[MT];
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const int64_t row = min(static_cast<int64_t>(t * 16 + i), p.m - 1);
-    x_row[t] = row * p.x_stride + g * 16;
-    xs[t] = p.xs + row * p.xs_row;
-  }
-  f4 acc[MT];
-#pragma unroll
-  for (int t = 0; t < MT; ++t) acc[t] = f4{0.f, 0.f, 0.f, 0.f};
-  constexpr int kDepth = MT == 1 ? 4 : 2;
-  const u4 zero = {0u, 0u, 0u, 0u};
-#pragma unroll 1
-  for (int b0 = wave; b0 < p.blocks; b0 += WAVES * kDepth) {
-    u4 wa[kDepth][2], xa[kDepth][MT][2];
-    float s[kDepth][MT];
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d) {
-      const int b = b0 + d * WAVES, at = b * kScaleBlock;
-      // (a piece past the end of k, and a block past the last, is zeros)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const bool in = at + g * 16 + h * 64 < p.k;
-        wa[d][h] = in ? __builtin_nontemporal_load(reinterpret_cast<const u4*>(w + w_row + at + h * 64)) : zero;
-#pragma unroll
-        for (int t = 0; t < MT; ++t) xa[d][t][h] = in ? *reinterpret_cast<const u4*>(p.x + x_row[t] + at + h * 64) : zero;
-      }
-      const int bb = min(b, p.blocks - 1);
-      const float sw = ws[bb * p.ws_block];
-#pragma unroll
-      for (int t = 0; t < MT; ++t) s[d][t] = b < p.blocks ? xs[t][bb * p.xs_block] * sw : 0.f;
-    }
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d) {
-      if (b0 + d * WAVES >= p.blocks) break;
-      const Frag<EXACT> wf(wa[d][0], wa[d][1]);
-#pragma unroll
-      for (int t = 0; t < MT; ++t) acc[t] += block_sums(wf, Frag<EXACT>(xa[d][t][0], xa[d][t][1])) * s[d][t];
-    }
-  }
-#pragma unroll
-  for (int t = 0; t < MT; ++t) red[wave][t][lane] = acc[t];
-  __syncthreads();
-  for (int t = wave; t < MT; t += WAVES) {
-    f4 v = red[0][t][lane];
-#pragma unroll
-    for (int o = 1; o < WAVES; ++o) v += red[o][t][lane];
-    store4(p, t * 16 + i, n0 + 4 * g, v);
-  }
-}
-
 // 64 lanes x 16 bytes from memory to LDS, past the registers: lane l's go to
 // dst + 16 l. M0 holds the place in LDS; the compiler does not track it, and
 // nothing else here uses it.
@@ -309,7 +245,109 @@ __device__ __forceinline__ void lds_dma4(const float* base, uint32_t offset, uin
 }
 #pragma clang diagnostic pop
 
-typedef const float __attribute__((address_space(4))) * scalar_ptr;  // read through the scalar cache
+// Few rows: a workgroup takes 16 outputs, its wavefronts every WAVES-th block of k
+// each; their sums are added in LDS in the order of the wavefronts. A block's
+// codes come to LDS, kRing blocks a wavefront on their way, and only from there
+// to the lanes that multiply them: neighbouring lanes hold neighbouring rows, and a
+// load of 16 bytes from each costs the cache 64 accesses instead of 16 (16 rows x
+// 5120 x 17408 34 us, with the memory's rate reached by neither more wavefronts
+// nor more loads on their way). A wavefront's part of LDS is its own: no barrier.
+template <int MT, int WAVES, bool EXACT>
+__global__ __launch_bounds__(WAVES * 64) void few_rows_kernel(const ProductParams p) {
+  constexpr int kRing = 2, kTile = 16 * kScaleBlock;
+  struct Slot {
+    uint8_t w[kTile], x[MT][kTile];
+    float scales[64];  // of all rows of x
+  };
+  constexpr int kLoads = 2 + 2 * MT + 1;
+  __shared__ union {
+    alignas(16) Slot ring[WAVES][kRing];
+    f4 red[WAVES][MT][64];
+  } sh;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+  const int i = lane & 15, g = lane >> 4;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
+  const uint8_t* w = p.w + n0 * p.w_stride;
+  const scalar_ptr ws = (scalar_ptr)(p.ws + n0 / kScaleBlock * p.ws_row);
+  // what a lane brings: of rows lane / 8 and 8 + lane / 8 of a tile, one piece
+  const uint32_t piece = ((lane & 7) ^ (lane >> 3)) * 16;
+  uint32_t from_w[2], from_x[MT][2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    from_w[h] = static_cast<uint32_t>(min(static_cast<int64_t>(h * 8 + lane / 8), p.n - 1 - n0) * p.w_stride) + piece;
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+      from_x[t][h] = static_cast<uint32_t>(min(static_cast<int64_t>(t * 16 + h * 8 + lane / 8), p.m - 1) * p.x_stride) + piece;
+  }
+  const uint32_t from_s = static_cast<uint32_t>(min(static_cast<int64_t>(lane), p.m - 1) * p.xs_row * 4);
+  const uint32_t ring0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_void)(&sh.ring[wave][0])));
+  const auto bring = [&](int b, int slot) {
+    const uint32_t to = __builtin_amdgcn_readfirstlane(ring0 + slot * static_cast<uint32_t>(sizeof(Slot)));
+    const int64_t at = static_cast<int64_t>(b) * kScaleBlock;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      lds_dma(w + at, from_w[h], to + h * 1024);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) lds_dma(p.x + at, from_x[t][h], to + (1 + t) * kTile + h * 1024);
+    }
+    lds_dma4(p.xs + b * p.xs_block, from_s, to + (1 + MT) * kTile);
+  };
+  f4 acc[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) acc[t] = f4{0.f, 0.f, 0.f, 0.f};
+  const int slot0 = i * kScaleBlock + ((g ^ (i & 7)) * 16), slot1 = i * kScaleBlock + (((g + 4) ^ (i & 7)) * 16);
+  const auto frag = [&](const uint8_t* tile) {
+    return Frag<EXACT>(*reinterpret_cast<const u4*>(tile + slot0), *reinterpret_cast<const u4*>(tile + slot1));
+  };
+  const int whole = p.k / kScaleBlock;  // blocks that are not cut by the end of k
+  static_assert(kRing == 2, "the loop below keeps one block on its way");
+  if (wave < whole) bring(wave, 0);
+  int slot = 0;
+#pragma unroll 1
+  for (int b = wave; b < whole; b += WAVES, slot ^= 1) {
+    if (b + WAVES < whole) {
+      bring(b + WAVES, slot ^ 1);
+      __builtin_amdgcn_s_waitcnt(vmcnt_only(kLoads));
+    } else {
+      __builtin_amdgcn_s_waitcnt(vmcnt_only(0));
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    const Slot& r = sh.ring[wave][slot];
+    const float sw = ws[b * p.ws_block];
+    const Frag<EXACT> wf = frag(r.w);
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[t] += block_sums(wf, frag(r.x[t])) * (r.scales[t * 16 + i] * sw);
+    // (the reads are over before their place is asked to be filled again)
+    __builtin_amdgcn_s_waitcnt(lgkmcnt_only(0));
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+  if (whole < p.blocks && whole % WAVES == wave) {
+    // the short last block, piece by piece: those past the end of k are zeros
+    const int64_t at = static_cast<int64_t>(whole) * kScaleBlock;
+    const u4 zero = {0u, 0u, 0u, 0u};
+    const auto short_frag = [&](const uint8_t* row) {
+      return Frag<EXACT>(at + g * 16 < p.k ? *reinterpret_cast<const u4*>(row + at + g * 16) : zero,
+                         at + g * 16 + 64 < p.k ? *reinterpret_cast<const u4*>(row + at + g * 16 + 64) : zero);
+    };
+    const float sw = ws[whole * p.ws_block];
+    const Frag<EXACT> wf = short_frag(w + min(static_cast<int64_t>(i), p.n - 1 - n0) * p.w_stride);
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const int64_t row = min(static_cast<int64_t>(t * 16 + i), p.m - 1);
+      acc[t] += block_sums(wf, short_frag(p.x + row * p.x_stride)) * (p.xs[row * p.xs_row + whole * p.xs_block] * sw);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int t = 0; t < MT; ++t) sh.red[wave][t][lane] = acc[t];
+  __syncthreads();
+  for (int t = wave; t < MT; t += WAVES) {
+    f4 v = sh.red[0][t][lane];
+#pragma unroll
+    for (int o = 1; o < WAVES; ++o) v += sh.red[o][t][lane];
+    store4(p, t * 16 + i, n0 + 4 * g, v);
+  }
+}
 
 // Many rows: MW x NW wavefronts of TM x TN tiles of 16 x 16 each. Both
 // operands' 128 bytes of a block go to LDS, the next block's while this one is
@@ -494,10 +532,13 @@ template <int MT, bool EXACT>
 hipError_t launch_few(int waves, uint32_t grid, const ProductParams& p, hipStream_t stream) {
   switch (waves) {
     case 4: few_rows_kernel<MT, 4, EXACT><<<dim3(grid), dim3(256), 0, stream>>>(p); break;
-    case 8: few_rows_kernel<MT, 8, EXACT><<<dim3(grid), dim3(512), 0, stream>>>(p); break;
+    case 8:
+      if constexpr (MT < 4) few_rows_kernel<MT, 8, EXACT><<<dim3(grid), dim3(512), 0, stream>>>(p);
+      else return hipErrorInvalidValue;
+      break;
     default:
-      if constexpr (MT == 4) return hipErrorInvalidValue;  // too many registers for 16 wavefronts
-      else few_rows_kernel<MT, 16, EXACT><<<dim3(grid), dim3(1024), 0, stream>>>(p);
+      if constexpr (MT == 1) few_rows_kernel<MT, 16, EXACT><<<dim3(grid), dim3(1024), 0, stream>>>(p);
+      else return hipErrorInvalidValue;
   }
   return hipGetLastError();
 }

@@ -36,7 +36,7 @@ bool plan_fp8_block(int64_t m, int64_t n, int64_t k, Fp8BlockPlan* p) {
   if (m <= 64) {
     p->m_tiles = static_cast<int>(std::max<int64_t>(1, ceil_div(m, 16)));
     p->waves = 4;
-    while (p->waves < (p->m_tiles == 4 ? 8 : 16) && ceil_div(n, 16) * p->waves < 2048 && p->blocks >= 8 * p->waves) p->waves *= 2;
+    while (p->waves < few_rows_waves(p->m_tiles) && ceil_div(n, 16) * p->waves < 2048 && p->blocks >= 8 * p->waves) p->waves *= 2;
   } else {
     // Tiles of 256 x 256, one a compute unit, where they come in whole rounds of 256; the
     // outputs of the last round that would not be full go in tiles of 128 x 128. (fp32

@@ -9,6 +9,10 @@ namespace qpn {
 
 constexpr int kScaleBlock = 128;  // elements along k (and rows of a weight) under one scale
 
+// Wavefronts of a few-rows workgroup, at most: two blocks each of both operands
+// have to fit LDS.
+constexpr int few_rows_waves(int m_tiles) { return m_tiles == 1 ? 16 : m_tiles < 4 ? 8 : 4; }
+
 // The shape of a block product, chosen by plan_fp8_block.
 struct Fp8BlockPlan {
   int m_tiles;       // > 0: a wavefront takes all rows, this many tiles of 16; 0: tiles in LDS

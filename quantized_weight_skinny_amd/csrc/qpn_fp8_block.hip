@@ -460,9 +460,8 @@ __global__ __launch_bounds__(MW * NW * 64, 2) void many_rows_kernel(const Produc
     xf[0] = frag(xt);
 #pragma unroll
     for (int u = 0; u < TN; ++u) wf[u] = frag(wt + u * 16 * kScaleBlock);
-    f4 s[TM / 4];
-#pragma unroll
-    for (int t = 0; t < TM / 4; ++t) s[t] = *reinterpret_cast<const f4*>(&scales[buf][(wm * 16 + i) * TM + t * 4]) * sw;
+    typedef float row_scales __attribute__((ext_vector_type(TM)));
+    const row_scales s = *reinterpret_cast<const row_scales*>(&scales[buf][(wm * 16 + i) * TM]) * sw;
     const bool more = b + 1 < b1, whole = (b + 2) * kScaleBlock <= p.k;
     if (more) {
       bring_scales(b + 1, buf ^ 1);
@@ -483,7 +482,7 @@ __global__ __launch_bounds__(MW * NW * 64, 2) void many_rows_kernel(const Produc
       for (int u = 0; u < TN; ++u) {
         if (t < TM) sums[t & 1][u] = block_sums(wf[u], xf[t & 1]);
         if (t > 0) {
-          acc[t - 1][u] += sums[(t - 1) & 1][u] * s[(t - 1) / 4][(t - 1) % 4];
+          acc[t - 1][u] += sums[(t - 1) & 1][u] * s[t - 1];
           asm volatile("" : "+v"(acc[t - 1][u]));  // (here: the compiler would gather them behind the loads)
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -613,20 +612,25 @@ hipError_t launch_fp8_block_gemm(const qpn_fp8_block_gemm_args& a, const Fp8Bloc
     p.n_first = first;
     p.tiles = static_cast<int32_t>((a.m + tile - 1) / tile * ((last - first + tile - 1) / tile));
     const dim3 grid(static_cast<uint32_t>((p.tiles + 7) / 8 * 8), static_cast<uint32_t>(plan.splits));
-    if (exact)  // (16 fp16 fragments beside 128 sums would not fit the registers)
-      many_rows_kernel<2, 2, 4, 4, true><<<grid, dim3(256), 0, stream>>>(p);
-    else if (tile == 256)
+    if (tile == 256)
       many_rows_kernel<2, 4, 8, 4, false><<<grid, dim3(512), 0, stream>>>(p);
-    else
+    else if (tile == 128 && exact)
+      many_rows_kernel<2, 2, 4, 4, true><<<grid, dim3(256), 0, stream>>>(p);
+    else if (tile == 128)
       many_rows_kernel<2, 2, 4, 4, false><<<grid, dim3(256), 0, stream>>>(p);
+    else if (exact)
+      many_rows_kernel<2, 2, 2, 2, true><<<grid, dim3(256), 0, stream>>>(p);
+    else
+      many_rows_kernel<2, 2, 2, 2, false><<<grid, dim3(256), 0, stream>>>(p);
     return hipGetLastError();
   };
+  // (fp32 results: 16 fp16 fragments beside 128 sums would not fit the registers)
   if (!exact && plan.wide > 0) {
     const hipError_t e = launch(256, 0, std::min(plan.wide, a.n));
     if (e != hipSuccess || plan.wide >= a.n) return e;
     return launch(128, plan.wide, a.n);
   }
-  hipError_t e = launch(128, 0, a.n);
+  hipError_t e = launch(plan.tile, 0, a.n);
   if (e != hipSuccess || plan.splits == 1) return e;
   const int64_t quads = a.m * ((a.n + 3) / 4);
   join_kernel<<<dim3(static_cast<uint32_t>((quads + 255) / 256)), dim3(256), 0, stream>>>(p);

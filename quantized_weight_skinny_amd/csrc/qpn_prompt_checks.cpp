@@ -47,10 +47,15 @@ bool plan_fp8_block(int64_t m, int64_t n, int64_t k, Fp8BlockPlan* p) {
       p->wide = left > kComputeUnits * 3 / 4 ? n : rounds * kComputeUnits / m_tiles * 256;
       p->wide = std::min(p->wide, n);
     }
-    const int64_t tiles = ceil_div(m, 128) * ceil_div(n, 128);
+    // Tiles of 64 x 64 where there would be fewer of 128 x 128 than compute units.
+    int64_t tiles = ceil_div(m, 128) * ceil_div(n, 128);
+    p->tile = tiles < kComputeUnits ? 64 : 128;
     if (tiles > kMaxGroups) return false;
-    if (tiles < 256)
-      p->splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(512 / std::max<int64_t>(1, tiles), p->blocks / 8)));
+    if (p->tile == 64) {
+      tiles = ceil_div(m, 64) * ceil_div(n, 64);
+      if (tiles < kComputeUnits)
+        p->splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(512 / std::max<int64_t>(1, tiles), p->blocks / 8)));
+    }
   }
   if (ceil_div(n, 16) > kMaxGroups || ceil_div(m * p->blocks, 16) > kMaxGroups) return false;
   p->code_bytes = round256(static_cast<size_t>(m) * k);

@@ -17,7 +17,8 @@ constexpr int few_rows_waves(int m_tiles) { return m_tiles == 1 ? 16 : m_tiles <
 struct Fp8BlockPlan {
   int m_tiles;       // > 0: a wavefront takes all rows, this many tiles of 16; 0: tiles in LDS
   int waves;         // wavefronts of a workgroup that share k (m_tiles > 0)
-  int64_t wide;      // outputs up to here in tiles of 256 x 256, the others 128 x 128 (fp32 results: all of them)
+  int tile;          // 128 or 64: rows and outputs of an LDS tile
+  int64_t wide;      // outputs up to here in tiles of 256 x 256 instead (fp32 results: none)
   int splits;        // k ranges, each to partial sums of its own; 1: none
   int blocks;        // ceil(k / 128)
   size_t code_bytes, scale_bytes, partial_bytes, total_bytes;

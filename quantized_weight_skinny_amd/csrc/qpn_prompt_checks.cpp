@@ -24,8 +24,6 @@ bool stride_ok(int64_t s) { return s >= 0 && s <= kMaxStride; }
 
 size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
 }  // namespace
 
 bool plan_fp8_block(int64_t m, int64_t n, int64_t k, Fp8BlockPlan* p) {

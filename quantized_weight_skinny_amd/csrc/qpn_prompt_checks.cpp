@@ -45,14 +45,19 @@ bool plan_fp8_block(int64_t m, int64_t n, int64_t k, Fp8BlockPlan* p) {
       p->wide = left > kComputeUnits * 3 / 4 ? n : rounds * kComputeUnits / m_tiles * 256;
       p->wide = std::min(p->wide, n);
     }
-    // Tiles of 64 x 64 where there would be fewer of 128 x 128 than compute units.
+    // Tiles of 64 x 64 where there would be fewer of 128 x 128 than compute units (777 x 1795
+    // x 1296, 105 or 377 of them: 27 us or 20), and the blocks split where even those are
+    // few: up to two workgroups a compute unit, or up to four where there are so many blocks
+    // that the join is little beside them (200 x 5120 x 17408, 320 tiles of 136 blocks: whole
+    // 83 us, in 3 splits 57, in 4 63; 100 x 7168 x 5120, 224 of 40: in 2 splits 25, in 4 27).
     int64_t tiles = ceil_div(m, 128) * ceil_div(n, 128);
     p->tile = tiles < kComputeUnits ? 64 : 128;
     if (tiles > kMaxGroups) return false;
     if (p->tile == 64) {
       tiles = ceil_div(m, 64) * ceil_div(n, 64);
-      if (tiles < kComputeUnits)
-        p->splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(512 / std::max<int64_t>(1, tiles), p->blocks / 8)));
+      const int64_t groups = (p->blocks >= 64 ? 4 : 2) * kComputeUnits;
+      if (tiles <= groups / 2)
+        p->splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(groups / std::max<int64_t>(1, tiles), p->blocks / 8)));
     }
   }
   if (ceil_div(n, 16) > kMaxGroups || ceil_div(m * p->blocks, 16) > kMaxGroups) return false;

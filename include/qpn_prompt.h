@@ -40,11 +40,14 @@ qpn_status qpn_fp8_block_quantize(const void* x_dev, int32_t dtype, int64_t rows
 
 /* y[m][n] = sum over k of (x code * x scale)[m][k] * (w code * w scale)[n][k],
  * x with a scale for each row and 128 columns, w with one for each 128 rows
- * and 128 columns (any fp32 scales). Products of codes are exact; the sum of a
- * block and the scaled sums of the blocks are fp32; y is rounded once. With x
- * of F16, BF16 or F32 it is quantized first, as by qpn_fp8_block_quantize with
- * block_rows 1, into the workspace. NaN codes make the outputs that they enter
- * NaN. */
+ * and 128 columns (any fp32 scales). A block's sum is scaled and added to the
+ * others' in fp32, and y is rounded once. For y of F32 the products of codes are
+ * exact and their sums fp32. For y of F16 or BF16 a block is summed by the 8-bit
+ * matrix instruction, which keeps its products to about 2^-11 of the block's
+ * largest: a result of random blocks is 1.4e-5 of itself off by that, a tenth
+ * and less of its rounding. With x of F16, BF16 or F32 it is quantized first, as
+ * by qpn_fp8_block_quantize with block_rows 1, into the workspace. NaN codes
+ * make the outputs that they enter NaN. */
 typedef struct {
   const void* x;          /* device: [m][k] of x_dtype, rows x_stride elements apart */
   const float* x_scales;  /* device: E4M3 x: [m][ceil(k / 128)] by strides; else NULL */

@@ -31,14 +31,22 @@ bool plan_fp8_block(int64_t m, int64_t n, int64_t k, Fp8BlockPlan* p) {
   *p = Fp8BlockPlan{};
   p->blocks = static_cast<int>(ceil_div(k, kScaleBlock));
   p->splits = 1;
-  if (m <= 64) {
+  // A wavefront takes all of up to 48 rows, or of up to 64 under a weight of up to 40 M codes
+  // (64 rows x 7168 x 5120: 18 us, in tiles 21; x 10240 x 5120: 24.5 and 23, x 5120 x 17408:
+  // 41 and 35; 48 rows x 17408 x 5120: 26 and 30).
+  if (m <= 48 || (m <= 64 && n * k <= 40 << 20)) {
     p->m_tiles = static_cast<int>(std::max<int64_t>(1, ceil_div(m, 16)));
     p->waves = 4;
-    while (p->waves < few_rows_waves(p->m_tiles) && ceil_div(n, 16) * p->waves < 2048 && p->blocks >= 8 * p->waves) p->waves *= 2;
+    // Up to 256 workgroups of 16 outputs, one a compute unit, share k among more wavefronts (16
+    // rows x 2048 x 17408: 12.3 us, with four 15.5; x 4096 x 16384 18.3 and 19.9; with more
+    // workgroups four are enough: x 5120 x 17408 21.6 and 20.1).
+    if (ceil_div(n, 16) <= kComputeUnits)
+      while (p->waves < few_rows_waves(p->m_tiles) && p->blocks >= 8 * p->waves) p->waves *= 2;
   } else {
     // Tiles of 256 x 256, one a compute unit, where they come in whole rounds of 256; the
-    // outputs of the last round that would not be full go in tiles of 128 x 128. (fp32
-    // results take those always.)
+    // outputs of the last round that would not be full go in tiles of 128 x 128 (2048 x 34816
+    // x 5120: 445 us, all in tiles of 256 453, all in tiles of 128 527; 1024 x 16384 x 4096,
+    // one whole round: 77 and 89). fp32 results take those always.
     const int64_t m_tiles = ceil_div(m, 256), n_tiles = ceil_div(n, 256), rounds = m_tiles * n_tiles / kComputeUnits;
     if (m >= 256 && rounds > 0) {
       const int64_t left = m_tiles * n_tiles - rounds * kComputeUnits;
@@ -184,7 +192,8 @@ qpn_status check_kv4_chunk(const qpn_kv4_cache* c, const qpn_kv4_chunk_args* a, 
 bool plan_logprobs(int32_t rows, int32_t vocab, int32_t top, LogprobsPlan* p) {
   if (rows < 0 || rows > (1 << 20) || vocab < 1 || vocab > (1 << 24) || top < 0 || top > 64 || top > vocab) return false;
   *p = LogprobsPlan{};
-  // as many slices as bring 2048 workgroups, 8 for each compute unit
+  // as many slices as bring 2048 workgroups, 8 for each compute unit (256 rows of 151936 with
+  // five first tokens: 45 us; 512 or 8192 workgroups 47)
   const int64_t wanted = rows > 0 ? ceil_div(2048, rows) : 1;
   const int64_t most = std::min<int64_t>(ceil_div(vocab, kLogprobsStep), top > 0 ? std::min(kLogprobsSlices, kLogprobsKeys / top) : kLogprobsSlices);
   const int64_t length = ceil_div(ceil_div(vocab, std::min(wanted, most)), kLogprobsStep) * kLogprobsStep;

@@ -38,13 +38,15 @@ int main() {
         CHECK(p.code_bytes >= static_cast<size_t>(m * k) && p.code_bytes % 256 == 0);
         CHECK(p.scale_bytes >= static_cast<size_t>(m * p.blocks * 4) && p.scale_bytes % 256 == 0);
         CHECK(qpn_fp8_block_workspace_bytes(m, n, k) == p.total_bytes);
-        if (m <= 64) {
+        CHECK(m > 48 || p.m_tiles > 0);
+        CHECK(m <= 64 || p.m_tiles == 0);
+        if (p.m_tiles > 0) {
           CHECK(p.m_tiles >= 1 && p.m_tiles <= 4 && p.m_tiles * 16 >= m && p.splits == 1);
           CHECK(p.waves == 4 || p.waves == 8 || p.waves == 16);
           CHECK(p.waves <= qpn::few_rows_waves(p.m_tiles) && ceil_div(n, 16) <= most_groups);
           CHECK(p.waves * 2 * ((1 + p.m_tiles) * 2048 + 256) <= 160 * 1024);  // its LDS
         } else {
-          CHECK(p.m_tiles == 0 && (p.tile == 64 || p.tile == 128));
+          CHECK(p.tile == 64 || p.tile == 128);
           CHECK(ceil_div(m, p.tile) * ceil_div(n, p.tile) + 8 <= most_groups + 8);
           CHECK(p.wide >= 0 && p.wide <= n && (p.wide == n || p.wide % 256 == 0));
           CHECK(p.wide == 0 || (m >= 256 && p.splits == 1 && p.tile == 128));

@@ -138,7 +138,8 @@ def test_quantizer_strides():
 
 SIZES = [(1, 1, 16), (1, 17, 128), (2, 130, 144), (16, 16, 2304), (17, 257, 1296), (33, 129, 112), (48, 40, 4096),
          (49, 300, 272), (64, 1, 128), (64, 513, 1040), (65, 128, 16), (128, 129, 128), (129, 127, 1296), (200, 64, 5120),
-         (300, 25700, 144), (257, 1000, 2048), (300, 33000, 272), (513, 25000, 144), (1100, 4000, 400), (70, 200, 9232)]
+         (300, 25700, 144), (257, 1000, 2048), (300, 33000, 272), (513, 25000, 144), (1100, 4000, 400), (70, 200, 9232),
+         (50, 10500, 4096), (130, 5500, 8192)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])

@@ -9,14 +9,15 @@
 // added in 64 bits.
 //
 // The first tokens are found in the same pass. Every wavefront keeps a list of
-// candidates above a bound of its own, which at least `top` of the elements it has
-// seen reach; a wavefront's elements come in the order of their index, so a
-// later one that equals the bound comes after these. The first bound is the
-// top-th largest of the lanes' maxima over a wavefront's first 1024 elements: some
-// (vocabulary / 4096) * top candidates follow for one wavefront of a row of no
-// order, and the list is cut back to `top` (by a search over the keys' bits,
-// with votes) when it passes twice that, which raises the bound. Rising rows, whose
-// every element passes, cost more and are no less right.
+// candidates above a bound, which at least `top` of the slice's elements so far
+// reach; a wavefront's elements come in the order of their index, so a later one
+// that equals the bound comes after these. The first bound is the top-th largest of
+// all lanes' maxima over the slice's first 4096 elements: a fourth of the candidates
+// follow that bounds from a wavefront's own 1024 would let through (64 rows of 50021
+// with 64 first tokens 26 us, with such bounds 39; 255 of 151936 with twenty 49 and
+// 57). A list is cut back to `top` (by a search over the keys' bits, with votes)
+// when it passes twice that, which raises the bound. Rising rows, whose every
+// element passes, cost more and are no less right.
 //
 // What bounds it: some 17 vector instructions an element, exponential and
 // comparisons among them: 2048 rows of 151936 bf16 with five first tokens 153 to 190
@@ -205,6 +206,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_slices_kernel(const Logprob
   __shared__ Stat joined[kWaves];
   __shared__ uint64_t lists[TOP ? kWaves : 1][kList + kAtOnce];
   __shared__ int counts[kWaves];
+  __shared__ uint32_t maxima[TOP ? kThreads : 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   const int row = blockIdx.x / p.slices, slice = blockIdx.x - row * p.slices;
   const T* x0 = static_cast<const T*>(p.a.logits) + row * p.a.row_stride;
@@ -244,7 +246,8 @@ __global__ __launch_bounds__(kThreads) void logprobs_slices_kernel(const Logprob
   // (a short list is cut by a hundred instructions, and a bound that rises early spares most steps)
   const int enough = min(2 * p.a.top + 8, kList);
 
-  for (int at = at0; at < end; at += kWaveStep * kWaves) {
+  // (each wavefront takes a first step, of -inf alone where it has no elements)
+  for (int at = at0; at < end || (TOP && first); at += kWaveStep * kWaves) {
     float x[kEach];
 #pragma unroll
     for (int j = 0; j < kPieces; ++j) widen_piece<T>(raw[j], &x[j * kPiece]);
@@ -289,13 +292,20 @@ __global__ __launch_bounds__(kThreads) void logprobs_slices_kernel(const Logprob
     if constexpr (TOP) {
       bool equal = false;  // elements that equal the bound count
       if (first) {
-        // the upper 16 bits of the top-th largest of the lanes' maxima
-        const uint32_t mine = order_of(most);
+        // the upper 16 bits of the top-th largest of all lanes' maxima
+        maxima[threadIdx.x] = order_of(most);
+        __syncthreads();
+        uint32_t each[kWaves];
+#pragma unroll
+        for (int o = 0; o < kWaves; ++o) each[o] = maxima[o * 64 + lane];
         uint32_t b = 0;
 #pragma unroll 1
         for (int bit = 31; bit >= 16; --bit) {
           const uint32_t next = b | 1u << bit;
-          if (static_cast<int>(__popcll(__ballot(mine >= next))) >= p.a.top) b = next;
+          int reached = 0;
+#pragma unroll
+          for (int o = 0; o < kWaves; ++o) reached += static_cast<int>(__popcll(__ballot(each[o] >= next)));
+          if (reached >= p.a.top) b = next;
         }
         if (b > kMinusInf) bound = value_of(b), equal = true;
         first = false;

@@ -20,10 +20,10 @@
 // element passes, cost more and are no less right.
 //
 // What bounds it: some 17 vector instructions an element, exponential and
-// comparisons among them: 2048 rows of 151936 bf16 with five first tokens 153 to 190
-// us, 3.3 to 4 TB/s, where the bytes alone take 101. Small calls are two launches and
-// their latency: one row of 151936 with twenty 19 us (9.4 + 10.7 for the kernels), 37
-// of 50021 fp32 16 us (5.3 + 4.2).
+// comparisons among them: 2048 rows of 151936 bf16 with five first tokens 149 to 186
+// us, 3.3 to 4.2 TB/s, where the bytes alone take 101. Small calls are two launches and
+// their latency: one row of 151936 with twenty 19 us (8.2 + 10.2 for the kernels), 37
+// of 50021 fp32 16 us (4.9 + 3.9).
 #include "qpn_decode_internal.hpp"
 #include "qpn_device.hpp"
 #include "qpn_prompt_internal.hpp"

@@ -193,7 +193,7 @@ bool plan_logprobs(int32_t rows, int32_t vocab, int32_t top, LogprobsPlan* p) {
   if (rows < 0 || rows > (1 << 20) || vocab < 1 || vocab > (1 << 24) || top < 0 || top > 64 || top > vocab) return false;
   *p = LogprobsPlan{};
   // as many slices as bring 2048 workgroups, 8 for each compute unit (256 rows of 151936 with
-  // five first tokens: 45 us; 512 or 8192 workgroups 47)
+  // five first tokens: 45 us, with 512 or 8192 workgroups 47)
   const int64_t wanted = rows > 0 ? ceil_div(2048, rows) : 1;
   const int64_t most = std::min<int64_t>(ceil_div(vocab, kLogprobsStep), top > 0 ? std::min(kLogprobsSlices, kLogprobsKeys / top) : kLogprobsSlices);
   const int64_t length = ceil_div(ceil_div(vocab, std::min(wanted, most)), kLogprobsStep) * kLogprobsStep;

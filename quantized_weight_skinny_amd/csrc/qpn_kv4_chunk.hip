@@ -188,7 +188,7 @@ struct Tiles {
   static constexpr int kKeyStride = DIM + 8;
   alignas(16) uint16_t k[kTokens * kKeyStride];
   alignas(16) uint16_t v[DIM * kTokens];
-  uint32_t odd[2];  // new tokens of the tile whose values hold inf or NaN
+  uint32_t odd[2];  // tokens of the 64 whose values hold inf or NaN, where some row may not see them
 };
 
 // The place of quad q (tokens 4 q .. 4 q + 3) in element d's row of V^T.
@@ -455,7 +455,8 @@ __global__ __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) void kv4_chunk_kernel
       }
       vs = *reinterpret_cast<const uint32_t*>(seg + page * DIM + page * (DIM / 16) + off / 4 * (DIM / 4) + (e * DIM / 256) * 4);
     };
-    const auto store_cached = [&](uint64_t held) {
+    // `guard`: some row may not see some token that is there, so a value scale of NaN must not meet its p of 0
+    const auto store_cached = [&](uint64_t held, bool guard) {
 #pragma unroll
       for (int j = 0; j < kKeyUnits; ++j) {
         const int unit = j * kThreads + tid, t = unit / kPerToken, part = unit % kPerToken;
@@ -469,8 +470,16 @@ __global__ __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) void kv4_chunk_kernel
       // tokens that are not there have scales of 0, whatever the cache holds: their p is 0, and must meet no NaN
       const int qd = tid / 16, e = tid % 16;
       const uint32_t there = static_cast<uint32_t>(held >> (4 * qd)) & 15u;
-      const uint32_t scales = vs & ((there & 1u) * 0xFFu | (there >> 1 & 1u) * 0xFF00u | (there >> 2 & 1u) * 0xFF0000u |
-                                    (there >> 3) * 0xFF000000u);
+      uint32_t scales = vs & ((there & 1u) * 0xFFu | (there >> 1 & 1u) * 0xFF00u | (there >> 2 & 1u) * 0xFF0000u |
+                              (there >> 3) * 0xFF000000u);
+      if (guard) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if ((scales >> (8 * x) & 0x7Fu) == 0x7Fu) {
+            scales &= ~(0xFFu << (8 * x));
+            atomicOr(&sh.odd[qd / 8], 1u << (qd % 8 * 4 + x));
+          }
+      }
       const h2 s01 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(scales, 1.0f, false);
       const h2 s23 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(scales, 1.0f, true);
       const auto put = [&](int d, uint32_t x, uint32_t y) {
@@ -528,8 +537,13 @@ __global__ __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) void kv4_chunk_kernel
     }
     uint64_t held = __ballot(pg >= 0);
     pg = page_of(cb + 1);
+    if (win) {
+      if (tid < 2) sh.odd[tid] = 0;
+      __syncthreads();
+    }
     for (int c = cb; c < ce; ++c) {
-      store_cached(held);
+      const bool guard = win != 0 && c * kTokens <= rt.len + q_last - win;
+      store_cached(held, guard);
       const uint64_t now = held;
       if (c + 1 < ce) {
         held = __ballot(pg >= 0);
@@ -542,7 +556,30 @@ __global__ __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) void kv4_chunk_kernel
         const bool whole = now == ~uint64_t(0) && (win == 0 || t0 > rt.len + w_last - win);
         step(Half<false>{}, f, whole, now, win ? rt.len + qi - win + 1 - t0 : 0, kTokens);
       }
+      bool struck = false;
+      if (guard) {
+        const uint32_t odd0 = sh.odd[0], odd1 = sh.odd[1];
+        struck = (odd0 | odd1) != 0;
+        // What was struck comes back for the rows that see it: 16 elements of NaN for each such scale.
+        for (uint64_t left = busy ? static_cast<uint64_t>(odd1) << 32 | odd0 : 0; left; left &= left - 1) {
+          const int t = c * kTokens + __builtin_ctzll(left), off = t & (page - 1);
+          const uint8_t* at = head_base + table[t >> a.page_shift] * a.page_bytes + page * DIM + page * (DIM / 16) +
+                              off / 4 * (DIM / 4) + off % 4;
+          if (t <= rt.len + qi - win) continue;
+#pragma unroll
+          for (int n = 0; n < kBlocks; ++n)
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+              if ((at[(n * 2 + y) * 4] & 0x7F) == 0x7F)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[n][y * 8 + e] = __builtin_nanf("");
+        }
+      }
       __syncthreads();
+      if (struck) {
+        if (tid < 2) sh.odd[tid] = 0;
+        __syncthreads();
+      }
     }
 #pragma unroll
     for (int n = 0; n < kBlocks; ++n) o[n] *= a.v_scale;

@@ -33,6 +33,8 @@
 // step's products in between this one's exponentials (1674, but heads of 256
 // spill: 980 instead of 275) gave nothing worth their cost.
 // One short run is its steps' latency: 5 tokens after 300 18 us.
+#include <algorithm>
+
 #include "qpn_device.hpp"
 #include "qpn_prompt_internal.hpp"
 #include "qpn_decode_internal.hpp"
@@ -49,6 +51,7 @@ constexpr int kThreads = 256, kRows = kChunkRows, kTokens = kChunkTokens;
 constexpr int kMinShare = 4;        // steps a share has at least
 constexpr float kNoToken = -1e30f;  // a row's reference before it has seen a token
 constexpr float kBias = 8.0f, kHeadroom = 15.0f;
+constexpr float kLeast = 1.17549435e-38f, kMost = 3.40282347e+38f;  // fp32's normal range
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
 
 struct ChunkParams {
@@ -535,6 +538,9 @@ __global__ __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) void kv4_chunk_kernel
                                         __uint_as_float(q[c][e] & 0xFFFF0000u) * down);
       f *= __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
     }
+    // (0 or inf times a score, -inf or 0, would be NaN. Products of queries and codes are below 2^36: a factor
+    // below the normal range makes them all as good as 0, and so does the least normal one)
+    f = fminf(fmaxf(f, kLeast), kMost);
     uint64_t held = __ballot(pg >= 0);
     pg = page_of(cb + 1);
     if (win) {
@@ -824,10 +830,10 @@ hipError_t launch_kv4_chunk(const qpn_kv4_cache& c, const qpn_kv4_chunk_args& x,
   a.table = x.table, a.table_stride = x.table_stride;
   a.kv_len = x.kv_len, a.q_start = x.q_start;
   a.batch = x.batch, a.rows = x.rows, a.max_q = x.max_q_len < x.rows ? x.max_q_len : x.rows;
-  constexpr int kMost = (1 << 30) + (1 << 21);  // no position is above 2^30 + 2^20, and one less this stays inside 32 bits
-  a.max_kv = x.max_kv_len, a.window = x.window < kMost ? x.window : kMost;
+  constexpr int kWindow = (1 << 30) + (1 << 21);  // no position is above 2^30 + 2^20, and one less this stays inside 32 bits
+  a.max_kv = x.max_kv_len, a.window = x.window < kWindow ? x.window : kWindow;
   a.tiles = p.tiles, a.groups = p.groups;
-  a.f = x.scale * kLog2e, a.k_scale = c.k_scale, a.v_scale = c.v_scale;
+  a.f = std::min(x.scale * kLog2e, kMost), a.k_scale = c.k_scale, a.v_scale = c.v_scale;
   a.cuts = static_cast<Cut*>(workspace);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.cut_bytes);
   return x.dtype == QPN_DT_BF16 ? launch_dim<true>(c.head_dim, a, stream) : launch_dim<false>(c.head_dim, a, stream);

@@ -40,6 +40,8 @@
 // the rest the launch (1 to 2), the shares' counting (3), first loads (3), joining
 // wavefronts (4) and pieces (6). At one row tile (one row, four wavefronts a
 // SIMD) 24 sequences' 180 MB take 39 us.
+#include <algorithm>
+
 #include "qpn_device.hpp"
 #include "qpn_decode_internal.hpp"
 
@@ -49,6 +51,7 @@ namespace {
 constexpr int kW = kAttnWaves;
 constexpr float kNoToken = -1e30f;  // a row's reference before it has seen a token
 constexpr float kBias = 8.0f, kHeadroom = 15.0f;
+constexpr float kLeast = 1.17549435e-38f, kMost = 3.40282347e+38f;  // fp32's normal range
 // What a run costs besides its tiles, in tiles: its queries, the first loads'
 // latency and the joining of the wavefronts (4 to 6 us where a tile takes 0.2
 // to 0.4). 48 ragged sequences 127 us with 0, 87 with 12, 81 with 20.
@@ -456,8 +459,11 @@ __global__ __launch_bounds__(kW * 64, attn_waves_per_simd(DIM, NQ)) void kv4_att
           return __builtin_bit_cast(h8, x);
         }
       };
+      // (kept in fp32's normal range: 0 or inf times a score, -inf or 0, would be NaN. Products of
+      // queries and codes are below 2^36, so that the least normal factor makes them all as good as 0.)
       const auto factor = [&](int e2) {
-        return BF16 ? a.f * __uint_as_float(static_cast<uint32_t>(127 + e2) << 23) : a.f;
+        if constexpr (!BF16) return a.f;
+        return fminf(fmaxf(a.f * __uint_as_float(static_cast<uint32_t>(127 + e2) << 23), kLeast), kMost);
       };
       // They are asked for before the first keys and values and made into
       // fragments while those come; in LDS, wavefront n does tile n for all four.
@@ -924,7 +930,8 @@ hipError_t launch_kv4_attention(const qpn_kv4_cache& c, const qpn_kv4_attention_
   // (no length is above 2^30; a position less the window stays inside 32 bits)
   a.max_kv = x.max_kv_len, a.window = x.window < (1 << 30) ? x.window : 1 << 30;
   a.row_tiles = p.row_tiles, a.groups = p.groups, a.min_share = p.min_share;
-  a.f = x.scale * 1.44269504088896341f * c.k_scale;
+  a.f = std::min(std::min(x.scale * 1.44269504088896341f, kMost) * c.k_scale, kMost);
+  if (x.dtype == QPN_DT_F16) a.f = std::max(a.f, kLeast);  // (bf16: with each row's power of two)
   a.v_scale = c.v_scale;
   a.cuts = static_cast<Cut*>(workspace);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.cut_bytes);

@@ -186,6 +186,14 @@ struct Frag<true> {
       : c{decode_fp8x8(c0[0], c0[1]), decode_fp8x8(c0[2], c0[3]), decode_fp8x8(c1[0], c1[1]), decode_fp8x8(c1[2], c1[3])} {}
 };
 
+// A lane's part of a block that begins at `at` less the lane's place, from memory: pieces past the end of k are zeros.
+template <bool EXACT>
+__device__ __forceinline__ Frag<EXACT> short_frag(const uint8_t* row, int64_t at, int k) {
+  const u4 zero = {0u, 0u, 0u, 0u};
+  return Frag<EXACT>(at < k ? *reinterpret_cast<const u4*>(row + at) : zero,
+                     at + 64 < k ? *reinterpret_cast<const u4*>(row + at + 64) : zero);
+}
+
 // The block's sums.
 __device__ __forceinline__ f4 block_sums(const Frag<true>& w, const Frag<true>& x) {
   f4 s = {0.f, 0.f, 0.f, 0.f};
@@ -199,6 +207,31 @@ __device__ __forceinline__ f4 block_sums(const Frag<false>& w, const Frag<false>
   const i8 b = {(int)b0[0], (int)b0[1], (int)b0[2], (int)b0[3], (int)b1[0], (int)b1[1], (int)b1[2], (int)b1[3]};
   // both operands E4M3, no scales of the instruction's own
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+}
+
+// A block's factor, x scale * w scale, serves its sums as it is where it is a normal number.
+// Where one is not, few rows take the way of add_scaled at once, and tiles once their loop is
+// over (the test takes an instruction a factor: 2048 x 34816 x 5120 402 us with and without it;
+// the other way inside the loop would have the compiler spill the tile of 256).
+__device__ __forceinline__ bool ordinary(float factor) {
+  return __builtin_amdgcn_classf(factor, 0x108);  // +normal, -normal
+}
+__device__ __forceinline__ bool finite_not_zero(float scale) {
+  return __builtin_amdgcn_classf(scale, 0x198);  // normal and subnormal
+}
+
+// acc += sums * xs * sw where it may not be: the scales' mantissas are multiplied first,
+// their exponents enter last, so that nothing leaves the range but a result that does.
+__device__ __forceinline__ void add_scaled(f4& acc, const f4& sums, float xs, float sw) {
+  const float factor = xs * sw;
+  const bool as_it_is = ordinary(factor);
+  const float m = __builtin_amdgcn_frexp_mantf(xs) * __builtin_amdgcn_frexp_mantf(sw);
+  const int e = __builtin_amdgcn_frexp_expf(xs) + __builtin_amdgcn_frexp_expf(sw);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float one = fmaf(sums[j], factor, acc[j]), other = acc[j] + __builtin_ldexpf(sums[j] * m, e);
+    acc[j] = as_it_is ? one : other;
+  }
 }
 
 // Four neighbouring outputs of one row.
@@ -321,25 +354,26 @@ __global__ __launch_bounds__(WAVES * 64) void few_rows_kernel(const ProductParam
     const float sw = ws[b * p.ws_block];
     const Frag<EXACT> wf = frag(r.w);
 #pragma unroll
-    for (int t = 0; t < MT; ++t) acc[t] += block_sums(wf, frag(r.x[t])) * (r.scales[t * 16 + i] * sw);
+    for (int t = 0; t < MT; ++t) {
+      const float xs = r.scales[t * 16 + i], factor = xs * sw;
+      const f4 sums = block_sums(wf, frag(r.x[t]));
+      if (__all(ordinary(factor))) acc[t] += sums * factor;
+      else add_scaled(acc[t], sums, xs, sw);
+    }
     // (the reads are over before their place is asked to be filled again)
     __builtin_amdgcn_s_waitcnt(lgkmcnt_only(0));
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
   if (whole < p.blocks && whole % WAVES == wave) {
     // the short last block, piece by piece: those past the end of k are zeros
-    const int64_t at = static_cast<int64_t>(whole) * kScaleBlock;
-    const u4 zero = {0u, 0u, 0u, 0u};
-    const auto short_frag = [&](const uint8_t* row) {
-      return Frag<EXACT>(at + g * 16 < p.k ? *reinterpret_cast<const u4*>(row + at + g * 16) : zero,
-                         at + g * 16 + 64 < p.k ? *reinterpret_cast<const u4*>(row + at + g * 16 + 64) : zero);
-    };
+    const int64_t at = static_cast<int64_t>(whole) * kScaleBlock + g * 16;
     const float sw = ws[whole * p.ws_block];
-    const Frag<EXACT> wf = short_frag(w + min(static_cast<int64_t>(i), p.n - 1 - n0) * p.w_stride);
+    const Frag<EXACT> wf = short_frag<EXACT>(w + min(static_cast<int64_t>(i), p.n - 1 - n0) * p.w_stride, at, p.k);
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
       const int64_t row = min(static_cast<int64_t>(t * 16 + i), p.m - 1);
-      acc[t] += block_sums(wf, short_frag(p.x + row * p.x_stride)) * (p.xs[row * p.xs_row + whole * p.xs_block] * sw);
+      add_scaled(acc[t], block_sums(wf, short_frag<EXACT>(p.x + row * p.x_stride, at, p.k)),
+                 p.xs[row * p.xs_row + whole * p.xs_block], sw);
     }
   }
   __syncthreads();
@@ -448,6 +482,7 @@ __global__ __launch_bounds__(MW * NW * 64, 2) void many_rows_kernel(const Produc
   const int slot0 = ((g ^ (i & 7)) * 16), slot1 = (((g + 4) ^ (i & 7)) * 16);
   constexpr int kLoads = kLoadsX + kLoadsW;
   float sw = 0.f;
+  bool plain = true;
   if (b0 < b1) {
     bring_scales(b0, 0);
     sw = ws[b0 * p.ws_block];
@@ -473,6 +508,8 @@ __global__ __launch_bounds__(MW * NW * 64, 2) void many_rows_kernel(const Produc
     for (int u = 0; u < TN; ++u) wf[u] = frag(wt + u * 16 * kScaleBlock);
     typedef float row_scales __attribute__((ext_vector_type(TM)));
     const row_scales s = *reinterpret_cast<const row_scales*>(&scales[buf][(wm * 16 + i) * TM]) * sw;
+#pragma unroll
+    for (int t = 0; t < TM; ++t) plain &= ordinary(s[t]);
     const bool more = b + 1 < b1, whole = (b + 2) * kScaleBlock <= p.k;
     if (more) {
       bring_scales(b + 1, buf ^ 1);
@@ -497,6 +534,45 @@ __global__ __launch_bounds__(MW * NW * 64, 2) void many_rows_kernel(const Produc
           asm volatile("" : "+v"(acc[t - 1][u]));  // (here: the compiler would gather them behind the loads)
         }
         __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+  // Factors outside the normal range were met: the wavefront's sums once more, from memory, unless the scales
+  // were zeros, infinities or NaN themselves.
+  if (!__all(plain)) {
+    const auto row_of = [&](int t) { return min(m0 + (wm * TM + t) * 16 + i, p.m - 1); };
+    bool left = false;
+    for (int b = b0; b < b1; ++b) {
+      const float one = ws[b * p.ws_block];
+      for (int t = 0; t < TM; ++t) {
+        const float xs = p.xs[row_of(t) * p.xs_row + b * p.xs_block];
+        left |= !ordinary(xs * one) && finite_not_zero(xs) && finite_not_zero(one);
+      }
+    }
+    if (__any(left)) {
+#pragma unroll
+      for (int t = 0; t < TM; ++t)
+#pragma unroll
+        for (int u = 0; u < TN; ++u) acc[t][u] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+      for (int b = b0; b < b1; ++b) {
+        const int64_t at = static_cast<int64_t>(b) * kScaleBlock + g * 16;
+        const float one = ws[b * p.ws_block];
+        Frag<EXACT> wf[TN];
+#pragma unroll
+        for (int u = 0; u < TN; ++u)
+          wf[u] = short_frag<EXACT>(p.w + min(n0 + (wn * TN + u) * 16 + i, p.n - 1) * p.w_stride, at, p.k);
+#pragma unroll
+        for (int t = 0; t < TM; ++t) {
+          const Frag<EXACT> xf = short_frag<EXACT>(p.x + row_of(t) * p.x_stride, at, p.k);
+          const float xs = p.xs[row_of(t) * p.xs_row + b * p.xs_block];
+#pragma unroll
+          for (int u = 0; u < TN; ++u) {
+            add_scaled(acc[t][u], block_sums(wf[u], xf), xs, one);
+            asm volatile("" : "+v"(acc[t][u]));
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
       }
     }
   }

@@ -140,8 +140,8 @@ qpn_status qpn_kv4_chunk_attention(const qpn_kv4_cache* cache, const qpn_kv4_chu
  * index. A token outside 0 .. vocab - 1 gives 0 and a rank of -1. NaN logits
  * count as -inf. Infinite logits share p = 1 among themselves; a row of -inf
  * alone gives log p = -inf and an entropy of 0. A temperature that is 0, below
- * or NaN counts as 1. Sums are fp32 over a few elements of a row and 64 bits
- * beyond. */
+ * or NaN counts as 1. Sums are fp32 over at most 128 elements of a row and 64
+ * bits beyond. */
 typedef struct {
   const void* logits;        /* device: [rows][vocab], rows row_stride elements apart */
   const int32_t* tokens;     /* device: [rows], or NULL with logprobs and rank NULL */

@@ -101,6 +101,8 @@ class BlockWeight:
     [ceil(n / 128), ceil(k / 128)], any strides. It keeps both as they are:
     nothing is copied or laid out anew."""
 
+    _FIXED = frozenset(("codes", "scales", "device", "n", "k", "_fields"))
+
     def __init__(self, codes, scales):
         _on_device(codes, "codes")
         dev = codes.device
@@ -112,6 +114,13 @@ class BlockWeight:
         sp, sr, sb = _block_scales(scales, (_blocks(n), _blocks(k)), "scales", dev)
         self.codes, self.scales, self.device, self.n, self.k = codes, scales, dev, n, k
         self._fields = (cp, sp, stride, sr, sb)
+
+    def __setattr__(self, name, value):
+        """Calls take the tensors' addresses and strides from here, so neither tensor
+        is replaced: their contents may change, other tensors are another weight."""
+        if name in self._FIXED and name in self.__dict__:
+            raise AttributeError(f"a weight's {name} does not change: make another weight of the other tensors")
+        super().__setattr__(name, value)
 
     @classmethod
     def quantize(cls, w):

@@ -45,7 +45,8 @@ qpn_status qpn_fp8_block_quantize(const void* x_dev, int32_t dtype, int64_t rows
  * exact and their sums fp32. For y of F16 or BF16 a block is summed by the 8-bit
  * matrix instruction, which keeps its products to about 2^-11 of the block's
  * largest: a result of random blocks is 1.4e-5 of itself off by that, a tenth
- * and less of its rounding. With x of F16, BF16 or F32 it is quantized first, as
+ * and less of its rounding, but where large products of a block cancel it is off by
+ * 2^-11 of what has cancelled (an fp32 y is not). With x of F16, BF16 or F32 it is quantized first, as
  * by qpn_fp8_block_quantize with block_rows 1, into the workspace. NaN codes
  * make the outputs that they enter NaN. */
 typedef struct {

@@ -15,9 +15,11 @@
 // 12 bits below the largest of them, not 24: blocks of normal values come out
 // 1.4e-5 of the result off (the 2-norms), measured, and the same for
 // v_mfma_f32_16x16x32_fp8_fp8. That is a tenth and less of the rounding to
-// fp16 or bf16, and too much for an fp32 result: there the codes are brought
-// to fp16, which holds them exactly, for v_mfma_f32_16x16x32_f16, whose sums are
-// fp32 (EXACT below), at half the rate.
+// fp16 or bf16; where large products of a block cancel it is 2^-11 of what has
+// cancelled, which may be more than the rounding. An fp32 result is the choice of a
+// caller who minds: there the codes are brought to fp16, which holds them exactly, for
+// v_mfma_f32_16x16x32_f16, whose sums are fp32 (EXACT below). At half the rate, 2048 x
+// 34816 x 5120 takes 674 us then instead of 397, which is why 16-bit results do not have it.
 #include <algorithm>
 
 #include "qpn_decode_internal.hpp"
@@ -107,8 +109,10 @@ struct QuantizeParams {
   int32_t blocks, load_vec, store_vec;
 };
 
-// A row's block of 128 is 16 lanes' (2048 x 5120 bf16: 10 us, 3 TB/s; a small call is a
-// launch, 3 us).
+// A row's block of 128 is 16 lanes', a load of 16 bytes each: 17408 x 5120 52 us (5.1
+// TB/s; a copy reaches 6.2), fp32 78 (5.7). 2048 x 5120 of bf16 take 8 to 11 us for 31 MB
+// that take 5 and 65 % of that in waiting, as its wavefronts are over after one
+// load; a small call is a launch, 3 us.
 template <int DT>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(const QuantizeParams a) {
   const int64_t t = static_cast<int64_t>(blockIdx.x) * 16 + threadIdx.x / 16;
@@ -129,7 +133,8 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const QuantizeParams
   if (threadIdx.x % 16 == 0) a.scales[row * a.scale_row_stride + block * a.scale_block_stride] = pow2(e2);
 }
 
-// 128 x 128 elements are one workgroup's.
+// 128 x 128 elements are one workgroup's: 17408 x 5120 of bf16 51 us (5.2 TB/s), fp32 82
+// (5.5), 151936 x 5120 428 (5.5).
 template <int DT>
 __global__ __launch_bounds__(256) void quantize_blocks_kernel(const QuantizeParams a) {
   __shared__ float top[4];
@@ -288,8 +293,10 @@ __device__ __forceinline__ void lds_dma4(const float* base, uint32_t offset, uin
 // nor more loads on their way). A wavefront's part of LDS is its own: no barrier.
 //
 // The weight's bytes bound it: one row x 34816 x 5120 29 us with the quantizer, 6.2
-// TB/s; 16 rows x 5120 x 17408 20 us, 4.5 TB/s (320 workgroups on 256 compute units).
-// Small calls are two launches: one row x 7168 x 5120 11 us for 6 us of bytes.
+// TB/s; 16 rows x 5120 x 17408 20 us where half of the weight is in the last-level cache
+// from the call before, 24 to 26 where all of it comes from memory (3.6 TB/s: 320
+// workgroups on 256 compute units, and the quantizer's launch). fp32 results cost 1 us
+// more there. Small calls are two launches: one row x 7168 x 5120 11 us for 6 us of bytes.
 template <int MT, int WAVES, bool EXACT>
 __global__ __launch_bounds__(WAVES * 64) void few_rows_kernel(const ProductParams p) {
   constexpr int kRing = 2, kTile = 16 * kScaleBlock;
@@ -400,11 +407,14 @@ __global__ __launch_bounds__(WAVES * 64) void few_rows_kernel(const ProductParam
 // of rows begins early enough to be whole (its rows are computed twice, to the same
 // bits), and one offset serves all of a thread's rows of x.
 //
-// What bounds it there: 1.65 to 1.85 PFLOP/s, the matrix cores 48 % busy, with the
-// clock down to 1.8 GHz under the card's power limit (the same call over zeros: 383 us
-// where it took 454). The rest of the cycles are the four multiply-adds a lane for
-// each instruction's sums. Tiles of 64 wait for memory: with four blocks in LDS
-// instead of two, fewer workgroups fit, and 777 x 1795 x 1296 takes 21 us, not 20.
+// What bounds it there (2048 x 34816 x 5120, 394 to 402 us with the quantizer, 1.85
+// PFLOP/s): of the cycles, matrix instructions take 46 % and vector ones 40 %, four
+// multiply-adds a lane for each instruction's sums among them, at a clock of 2.0 to 2.1
+// GHz under load (over zeros, which draw less power: 372 us where it took 397).
+// Tiles of 64 wait: matrix instructions 8 % and vector ones 15 % of the cycles at 777 x
+// 1795 x 1296, 19.5 us for an fp32 result, of which rows of an odd length cost 2.6
+// (16.9 at 1796) and fp16 instructions little (17.2 for bf16). With four blocks in LDS
+// instead of two, fewer workgroups fit: 21 us.
 //
 // Workgroups go round the eight dies. Each die takes an eighth of the tiles, row
 // tiles first: its 32 compute units read 8 x 4 tiles' rows between them rather

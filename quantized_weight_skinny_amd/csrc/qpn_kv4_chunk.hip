@@ -22,17 +22,25 @@
 // f = scale * log2(e) (* k_scale for the cache); v_scale multiplies O once,
 // between the cached and the new tokens.
 //
+// What is rounded, and why. The matrix instructions take 16-bit operands, so p is
+// rounded before its product with the values: to fp16 for cached tokens, whose values fp16
+// holds exactly, and to their own type for new ones. Taken apart into two such halves it
+// would need 16 more of a step's 32 matrix instructions, which are 38 % of the
+// cycles already. It adds 2e-4 (fp16) or 1.1e-3 (bf16) of a result to the rounding of the result
+// itself, 2.1e-4 or 1.6e-3: together 2.9e-4 and 2.0e-3, heads of 256 2.1e-3 (2-norms).
+//
 // What bounds it, at 2048 new tokens after 30000 (40 heads on 8 of 128, 1.3 Tflop):
-// 1505 to 1720 us, 0.8 PFLOP/s of the 1.35 that a large product reaches. The matrix
-// instructions take 41 % of the cycles and the vector ones (exponentials, the
-// decoding) 52 %, with little overlap; the clock is at 1.8 GHz under the card's power
-// limit (over zeros: 1336 us). 128 rows a workgroup and 64 tokens: 256 threads with
+// 1505 to 1560 us, 0.86 PFLOP/s of the 1.35 that a large product reaches. The matrix
+// instructions take 38 % of the cycles and the vector ones (exponentials, the
+// decoding) 49 %, with little overlap; the clock is at 2.0 GHz under load (over zeros,
+// which draw less power: 1356 us where it took 1514). Heads of 64: 1015 us, where exponentials
+// are twice as many for each product. 128 rows a workgroup and 64 tokens: 256 threads with
 // O, Q and P in registers, two workgroups a compute unit, so that one decodes while
-// the other multiplies. Two LDS buffers and one barrier a step (1724), a raised
-// priority around the products (1704 to 1750), more LDS reads ahead (1790) and the next
-// step's products in between this one's exponentials (1674, but heads of 256
-// spill: 980 instead of 275) gave nothing worth their cost.
-// One short run is its steps' latency: 5 tokens after 300 18 us.
+// the other multiplies. Where this took 1723 us, two LDS buffers and one barrier a step
+// took 1724, a raised priority around the products 1704 to 1750, more LDS reads ahead 1790
+// and the next step's products in between this one's exponentials 1674, but heads of
+// 256 spill then (980 instead of 275): none is worth its cost.
+// One short run is its steps' latency: 5 tokens after 300 19 us.
 #include <algorithm>
 
 #include "qpn_device.hpp"
@@ -48,7 +56,10 @@ typedef __bf16 b2 __attribute__((ext_vector_type(2)));
 typedef u4 u4_anywhere __attribute__((aligned(2)));
 
 constexpr int kThreads = 256, kRows = kChunkRows, kTokens = kChunkTokens;
-constexpr int kMinShare = 4;        // steps a share has at least
+// Steps a share has at least: every share of a run writes and joins a piece of it. With 1,
+// 2, 4, 8: 5 rows after 1000 tokens 16.7, 18.1, 20.7, 27 us; 60 after 3000 34, 34, 35, 39; 8
+// sequences of 1 to 100 after 100 to 3000 38, 38, 40, 49; 24 ragged ones 299, 297, 295, 294.
+constexpr int kMinShare = 4;
 constexpr float kNoToken = -1e30f;  // a row's reference before it has seen a token
 constexpr float kBias = 8.0f, kHeadroom = 15.0f;
 constexpr float kLeast = 1.17549435e-38f, kMost = 3.40282347e+38f;  // fp32's normal range
@@ -86,7 +97,9 @@ struct Sequence {
   int qs, ql, len, tiles, first, more;
 };
 
-// What a run costs besides its steps, in steps: queries, the first loads, the output.
+// What a run costs besides its steps, in steps: queries, the first loads, the output. 24
+// ragged sequences take 351 us with 0, 318 with 1, 296 with 3, 300 with 6; 8 of 1 to 100 rows after
+// 100 to 3000 47, 40, 40, 34; one of 2048 rows the same with all.
 constexpr int kRunCost = 3;
 
 __device__ __forceinline__ Sequence sequence(const ChunkParams& a, int b) {

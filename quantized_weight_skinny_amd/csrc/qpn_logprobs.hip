@@ -19,11 +19,11 @@
 // when it passes twice that, which raises the bound. Rising rows, whose every
 // element passes, cost more and are no less right.
 //
-// What bounds it: some 17 vector instructions an element, exponential and
-// comparisons among them: 2048 rows of 151936 bf16 with five first tokens 149 to 186
-// us, 3.3 to 4.2 TB/s, where the bytes alone take 101. Small calls are two launches and
-// their latency: one row of 151936 with twenty 19 us (8.2 + 10.2 for the kernels), 37
-// of 50021 fp32 16 us (4.9 + 3.9).
+// What bounds it: some 16 vector instructions an element, exponential and
+// comparisons among them: 2048 rows of 151936 bf16 with five first tokens 150 to 190
+// us, 3.3 to 4.1 TB/s, where the bytes alone take 101. Small calls are two launches and
+// their latency: one row of 151936 with twenty 18 us (8.0 + 10.5 for the kernels), 37
+// of 50021 fp32 16 us (5.0 + 3.9).
 #include "qpn_decode_internal.hpp"
 #include "qpn_device.hpp"
 #include "qpn_prompt_internal.hpp"

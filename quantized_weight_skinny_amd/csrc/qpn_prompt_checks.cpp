@@ -45,8 +45,9 @@ bool plan_fp8_block(int64_t m, int64_t n, int64_t k, Fp8BlockPlan* p) {
   } else {
     // Tiles of 256 x 256, one a compute unit, where they come in whole rounds of 256; the
     // outputs of the last round that would not be full go in tiles of 128 x 128 (2048 x 34816
-    // x 5120: 445 us, all in tiles of 256 453, all in tiles of 128 527; 1024 x 16384 x 4096,
-    // one whole round: 77 and 89). fp32 results take those always.
+    // x 5120: 387 us, all in tiles of 256 408, all in tiles of 128 488; 1024 x 16384 x 4096,
+    // one whole round: 72 and 84; with less than a round a long k would be better off, too:
+    // 2048 x 5120 x 17408 257 us, in its 160 tiles of 256 219). fp32 results take those of 128 always.
     const int64_t m_tiles = ceil_div(m, 256), n_tiles = ceil_div(n, 256), rounds = m_tiles * n_tiles / kComputeUnits;
     if (m >= 256 && rounds > 0) {
       const int64_t left = m_tiles * n_tiles - rounds * kComputeUnits;
@@ -54,10 +55,15 @@ bool plan_fp8_block(int64_t m, int64_t n, int64_t k, Fp8BlockPlan* p) {
       p->wide = std::min(p->wide, n);
     }
     // Tiles of 64 x 64 where there would be fewer of 128 x 128 than compute units (777 x 1795
-    // x 1296, 105 or 377 of them: 27 us or 20), and the blocks split where even those are
-    // few: up to two workgroups a compute unit, or up to four where there are so many blocks
-    // that the join is little beside them (200 x 5120 x 17408, 320 tiles of 136 blocks: whole
-    // 83 us, in 3 splits 57, in 4 63; 100 x 7168 x 5120, 224 of 40: in 2 splits 25, in 4 27).
+    // x 1296, 105 or 377 of them: 27 us or 20; 500 x 5120 x 5120, 160 or 640: 43 and 35; 100 x
+    // 34816 x 5120, with 272 of 128: 47, with 1088 of 64 59), and the blocks split where even
+    // those are few: up to two workgroups a compute unit, or up to four where there are so many
+    // blocks that the join is little beside them. In 1, 2, 3, 4, 6 and 8 splits: 200 x 5120 x
+    // 17408 (320 tiles of 136 blocks) 81, 57, 55, 62, 63, 67 us; 256 x 4096 x 8192 (256 of 64) 43, 33,
+    // 33, 34, 40, 45; 300 x 1024 x 16384 (80 of 128) 78, 48, 38, 34, 30, 31, in the 12 that this takes
+    // 33; 100 x 7168 x 5120 (224 of 40) 29, 25, 26, 27, 32, 34; 70 x 2048 x 4096 (64 of 32) 23, 19,
+    // 17, 16, 17, 18; not split: 500 x 5120 x 5120 35, 47, 52, 57; 100 x 17408 x 5120 32, 44, 44, 48.
+    // Tiles of 128 in their best number of splits: 53 (3), 33 (4), 35 (8), 26 (4), 19 (6).
     int64_t tiles = ceil_div(m, 128) * ceil_div(n, 128);
     p->tile = tiles < kComputeUnits ? 64 : 128;
     if (tiles > kMaxGroups) return false;
@@ -147,12 +153,15 @@ qpn_status plan_chunk(const qpn_kv4_cache* c, const qpn_kv4_chunk_args* a, Chunk
   // Steps of a run, at most. A run goes whole, a workgroup each, where it is over before a
   // join would be, or where there are many runs of no great length: heads of 256, 828 runs
   // of 18 steps 206 us whole and 275 in equal shares; heads of 128, 2600 runs of up to 152
-  // steps 485 us whole and 335 in shares, 640 of 500 steps 2120 and 1720.
+  // steps 485 us whole and 335 in shares, 640 of 500 steps 2120 and 1720. Short runs of 128
+  // elements a head, whole and shared: 8 runs (5 rows) of 2 steps 12.8 and 16.5 us, of 4 15.5 and
+  // 18.4, of 6 18.8 and 18.7, of 8 22.3 and 20.3, of 12 29 and 21; 512 runs of 4 steps 19 and 21, of
+  // 8 28 and 31, of 17 48 and 51; 96 runs (4 x 60 rows) of 4 18 and 32, of 8 25 and 35, of 12 32 and 37.
   int64_t steps = ceil_div(a->max_kv_len, kChunkTokens) + ceil_div(longest, kChunkTokens);
   if (a->window > 0) steps = std::min(steps, a->window / kChunkTokens + ceil_div(kChunkRows, group * kChunkTokens) + 2);
   const int64_t room = kComputeUnits * chunk_groups_per_unit(c->head_dim);
   const bool whole = steps <= 8 || (steps <= 64 && units >= 3 * room);
-  // (shares are not cut below four steps each)
+  // (shares are not cut below kMinShare of 4 steps each: see there)
   if (!whole) p->groups = static_cast<int>(std::min<int64_t>(room, ceil_div(units * ceil_div(steps, 4), 8) * 8));
   p->cut_bytes = static_cast<size_t>(p->groups) * 32;
   p->total_bytes = p->cut_bytes + static_cast<size_t>(p->groups) * 2 * kChunkRows * (c->head_dim + 2) * sizeof(float);

@@ -84,7 +84,10 @@ qpn_status qpn_kv4_copy_pages(const qpn_kv4_cache* cache, const int32_t* src_dev
  *   lse[row][head] = log sum_t exp(scale * q . k_t)            (fp32, may be NULL)
  * A row that sees no token (a length of 0, a position below 0) gets zeros and
  * -inf. A page index outside the pool holds no tokens: its positions are not
- * seen. Rows that no sequence has are not written. Cached values enter the
+ * seen. Rows that no sequence has are not written. What the cache holds for
+ * tokens past the end, or in front of the windows of all of a sequence's rows, has no
+ * effect; a NaN scale of a value (qpn_kv4_append writes none) that some of a
+ * sequence's rows see may reach its others. Cached values enter the
  * products exactly, all sums are fp32, and two factors are rounded to fp16:
  *  - q of bf16, scaled by a power of two that takes a row's largest element to
  *    2^15: elements keep their 8 bits down to 2^-32 of it, smaller ones are off

@@ -658,12 +658,13 @@ __global__ __launch_bounds__(kW * 64, attn_waves_per_simd(DIM, NQ)) void kv4_att
             tok + kTileTokens - 1 <= first_pos && (win == 0 || tok > last_pos - win) && !none0 && !none1;
         if (!whole) {
           // Scores of unseen tokens become -inf whatever the cache holds there,
-          // and the values of tokens past the end or of absent pages are zeroed:
-          // such bytes may decode to NaN, which a p of 0 would not remove. Bit b
-          // of a mask stands for token tok + 4 g + b.
+          // and the values of tokens past the end, of absent pages or in front of
+          // all rows' windows are zeroed: such bytes may decode to NaN, which a p of
+          // 0 would not remove. Bit b of a mask stands for token tok + 4 g + b.
           const int mine0 = tok + 4 * g;
           const auto up_to = [](int x) -> uint32_t { return x < 0 ? 0u : x >= 31 ? ~0u : (2u << x) - 1u; };
-          const uint32_t held = up_to(s.len - 1 - mine0) & ((none0 ? 0u : 0xFFFFu) | (none1 ? 0u : 0xFFFF0000u));
+          const uint32_t held = up_to(s.len - 1 - mine0) & (win ? ~up_to(first_pos - win - mine0) : ~0u) &
+                                ((none0 ? 0u : 0xFFFFu) | (none1 ? 0u : 0xFFFF0000u));
           const auto bit = [](uint32_t w, int b) {
             return static_cast<uint32_t>(static_cast<int32_t>(w << (31 - b)) >> 31);
           };
